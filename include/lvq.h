@@ -320,11 +320,108 @@ LVQ_API void lvq_pool_destroy(lvq_pool* pool);
 /* n free page ids into ids[0..n), lowest first; LVQ_ECAPACITY (nothing taken) if fewer than
  * n are free. */
 LVQ_API lvq_status lvq_pool_alloc(lvq_pool* pool, int32_t n, int32_t* ids);
-/* Returns n ids to the pool; LVQ_EINVAL (nothing returned) if an id is out of range, not
- * currently handed out, or repeated. */
+/* One holder of each of the n pages lets go; a page returns to the pool with its last holder
+ * (lvq_pool_alloc gives it one, lvq_pool_share more).  LVQ_EINVAL (nothing returned) if an id is
+ * out of range, not currently handed out, or repeated. */
 LVQ_API lvq_status lvq_pool_free(lvq_pool* pool, const int32_t* ids, int32_t n);
+/* One more holder of each of the n pages: a forked request's page list names its parent's full
+ * pages.  LVQ_EINVAL (nothing changed) as for lvq_pool_free. */
+LVQ_API lvq_status lvq_pool_share(lvq_pool* pool, const int32_t* ids, int32_t n);
+/* Holders of page id: 0 for a free page, -1 for a null pool or an id out of range. */
+LVQ_API int32_t lvq_pool_holders(const lvq_pool* pool, int32_t id);
+/* The pool's side of a compaction: page id becomes new_id[id] (n_pages entries, as
+ * lvq_plan_compaction writes them: -1 for a free page), holders and all.  LVQ_EINVAL (nothing
+ * changed) if a handed-out page has no new id, a free one has, or two have the same. */
+LVQ_API lvq_status lvq_pool_renumber(lvq_pool* pool, const int32_t* new_id);
 /* Free page ids (-1 for a null pool). */
 LVQ_API int32_t lvq_pool_available(const lvq_pool* pool);
+
+/* Plans a compaction of a pool of n_pages pages: the pages named by order[0 .. n_order) (a page
+ * named again, as shared pages are, keeps its first place) get the ids 0, 1, ... in that order.
+ * Host memory only, no pool involved.
+ *   new_id: n_pages entries, the new id of every page, -1 for one that order does not name.
+ *   moves: room for n_order + n_order / 2 pairs (source, destination), in the order and form
+ *     lvq_compact_pages carries them out; *n_moves receives their number.
+ * LVQ_EINVAL for a null pointer, a negative count or an id out of range (outputs then undefined);
+ * LVQ_ECAPACITY if host memory is short. */
+LVQ_API lvq_status lvq_plan_compaction(int32_t n_pages, const int32_t* order, int32_t n_order,
+                                       int32_t* new_id, int32_t* moves, int32_t* n_moves);
+
+/* Copies pages within the pool, in every (layer, block, head, K/V) (pool mode only, else
+ * LVQ_EUNSUPPORTED).  pairs: device int32 [n][2], (source, destination) physical pages, 8-byte
+ * aligned; no destination may be named twice or be a source of the same call.  A pair that is out
+ * of range sets LVQ_ECAPACITY in *dev_status and is skipped. */
+LVQ_API lvq_status lvq_copy_pages(const lvq_config* cfg, const lvq_layout* lay, int32_t n,
+                                  const int32_t* pairs, uint8_t* idx, int32_t* dev_status,
+                                  void* stream);
+
+/* Compacts the pool in place (pool mode only, else LVQ_EUNSUPPORTED), in every (layer, block,
+ * head, K/V), and rewrites the page table.
+ *   moves: device int32 [n_moves][2] from lvq_plan_compaction, 8-byte aligned.  They are carried
+ *     out in slabs of LVQ_MOVE_SLAB pairs, the reads of a slab before its writes; LVQ_PAGE_HOLD
+ *     names a page's worth of memory of the kernel's own (a cycle longer than a slab passes
+ *     through it).  Anything else out of range sets LVQ_ECAPACITY in *dev_status and is skipped.
+ *   new_id: device int32 [pool_pages] from the same plan.
+ *   page_table: cfg->page_table, writable.  Every entry that names a page becomes that page's
+ *     new id; the others stay.
+ * Pages that no move writes keep their contents. */
+#define LVQ_MOVE_SLAB 128
+#define LVQ_PAGE_HOLD (-1)
+LVQ_API lvq_status lvq_compact_pages(const lvq_config* cfg, const lvq_layout* lay, int32_t n_moves,
+                                     const int32_t* moves, const int32_t* new_id,
+                                     int32_t* page_table, uint8_t* idx, int32_t* dev_status,
+                                     void* stream);
+
+/* Forks request `parent`: every child becomes a copy of it, in one launch -- sink tokens and the
+ * live slots of the recent window (every layer, K/V and loop step), ctx_len and coded_len, and
+ * the coded tokens:
+ *   - pool mode: the child's page-table row names the parent's coded_tokens / 8 full pages (take
+ *     them with lvq_pool_share); where coded_tokens is not a multiple of 8 its next entry is
+ *     tail_pages[i] (one page of the child's own, from lvq_pool_alloc), into which the parent's
+ *     partial last page is copied; the rest of the row is -1.
+ *   - per-request streams: the parent's code pages are copied.
+ * Host arguments: children[0 .. n_children) (distinct, not the parent; n_children <= 256, else
+ * LVQ_EUNSUPPORTED), coded_tokens (the parent's coded_len), tail_pages[0 .. n_children) (NULL
+ * where no page is copied; distinct, in range).  page_table: cfg->page_table, writable (NULL
+ * outside pool mode).
+ * Device-side: LVQ_EINVAL in *dev_status if coded_len[parent] is not coded_tokens, LVQ_ECAPACITY
+ * if the parent's counters are outside the layout or its partial page is not in the page table;
+ * nothing is written then.  Slots of the window that hold no token, and requests that are not
+ * named, stay as they are. */
+LVQ_API lvq_status lvq_fork_requests(const lvq_config* cfg, const lvq_layout* lay, int32_t parent,
+                                     int32_t n_children, const int32_t* children,
+                                     int32_t coded_tokens, const int32_t* tail_pages,
+                                     int32_t* ctx_len, int32_t* coded_len, void* sink, void* ring,
+                                     uint8_t* idx, int32_t* page_table, int32_t* dev_status,
+                                     void* stream);
+
+/* Decode attention of loop step `step` of layer `layer` for a batch whose requests share coded
+ * prefixes: what lvq_decode_attention computes, with the shared tokens of a group of requests
+ * read, restored and rotated once for all the group's queries.
+ *   group_begin: device int32 [n_groups + 1], ascending from 0 to batch; group i holds the
+ *     requests [group_begin[i], group_begin[i + 1]).  A request on its own is a group of one.
+ *   group_tokens: device int32 [n_groups]: coded tokens 0 .. group_tokens[i] - 1 are the same in
+ *     all requests of group i.  Whole pages are shared: the value is rounded down to a multiple
+ *     of 8, and to no more than the smallest coded_len of the group.  In pool mode the requests'
+ *     page-table rows must name the same pages there (as lvq_fork_requests leaves them); a row
+ *     that does not sets LVQ_EINVAL in *dev_status.  Otherwise they are read from the group's
+ *     first request.
+ *   num_splits: every KV head's work is cut into num_splits parts of equal cost, a CTA each
+ *     (1 .. max_splits); 0 lets the library choose.
+ *   workspace: as for lvq_decode_attention, whose calls may share it (its counters stay zero).
+ * Other arguments as for lvq_decode_attention.  batch <= 512, else LVQ_EUNSUPPORTED.  Sums are
+ * taken in a fixed order: the same call gives the same bits.  A request whose counters are
+ * outside the layout, or page-table entries out of range: LVQ_ECAPACITY, as there; a group_begin
+ * that is not as described: LVQ_EINVAL (outputs then not meaningful). */
+LVQ_API lvq_status lvq_decode_attention_shared(const lvq_config* cfg, const lvq_layout* lay, int32_t layer,
+                                               int32_t step, int32_t batch, const void* q,
+                                               const int32_t* ctx_len, const int32_t* coded_len,
+                                               int32_t n_groups, const int32_t* group_begin,
+                                               const int32_t* group_tokens, const void* sink,
+                                               const void* ring, const uint8_t* idx, const void* cbp,
+                                               const float* rope, int32_t num_splits,
+                                               float* workspace, float* out, float* lse,
+                                               int32_t* dev_status, void* stream);
 
 /* Decode attention without a caller-supplied workspace.  The pages have no
  * counterpart of this entry point: it exists for callers that cannot allocate

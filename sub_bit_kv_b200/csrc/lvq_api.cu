@@ -124,6 +124,17 @@ lvq_status check_device() {
   return good ? LVQ_OK : LVQ_EDEVICE;
 }
 
+// Multiprocessors of the current device (0 if the query fails).
+int device_sms() {
+  static int count[kMaxDevices] = {};
+  int dev = -1, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < kMaxDevices && count[dev] > 0) return count[dev];
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < kMaxDevices) count[dev] = n;
+  return n;
+}
+
 lvq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? LVQ_OK : LVQ_ECUDA; }
 
 }  // namespace
@@ -281,6 +292,93 @@ lvq_status lvq_dequantize(const lvq_config* cfg, const lvq_layout* lay, int32_t 
                                        static_cast<cudaStream_t>(stream)));
 }
 
+lvq_status lvq_decode_attention_shared(const lvq_config* cfg, const lvq_layout* lay, int32_t layer, int32_t step,
+                                       int32_t batch, const void* q, const int32_t* ctx_len,
+                                       const int32_t* coded_len, int32_t n_groups, const int32_t* group_begin,
+                                       const int32_t* group_tokens, const void* sink, const void* ring,
+                                       const uint8_t* idx, const void* cbp, const float* rope, int32_t num_splits,
+                                       float* workspace, float* out, float* lse, int32_t* dev_status, void* stream) {
+  Geo g;
+  lvq_status s = check_all(cfg, lay, &g);
+  if (s != LVQ_OK) return s;
+  if (layer < 0 || layer >= g.L || step < 0 || step >= g.T || batch < 0 || batch > g.B || num_splits < 0 ||
+      num_splits > g.max_splits || n_groups < 0 || n_groups > batch || (batch > 0 && n_groups == 0))
+    return LVQ_EINVAL;
+  if (batch > kSharedMaxBatch) return LVQ_EUNSUPPORTED;
+  if (batch > 0) {
+    const void* ptrs[] = {q, ring, idx, cbp, rope, workspace, out, lse};
+    for (const void* p : ptrs)
+      if (!p || !aligned16(p)) return LVQ_EINVAL;
+    if (g.S > 0 && (!sink || !aligned16(sink))) return LVQ_EINVAL;
+    if (!ctx_len || !coded_len || !group_begin || !group_tokens) return LVQ_EINVAL;
+  }
+  if ((s = check_device()) != LVQ_OK) return s;
+  if (batch == 0) return LVQ_OK;
+  const int n_sm = device_sms();
+  if (n_sm < 1) return LVQ_ECUDA;
+  return cuda_status(launch_decode_shared(g, layer, step, batch, static_cast<const __nv_bfloat16*>(q), ctx_len, coded_len,
+                                          n_groups, group_begin, group_tokens, static_cast<const __nv_bfloat16*>(sink),
+                                          static_cast<const __nv_bfloat16*>(ring), idx,
+                                          static_cast<const __nv_bfloat16*>(cbp), rope, num_splits, workspace, out, lse,
+                                          dev_status, n_sm, static_cast<cudaStream_t>(stream)));
+}
+
+lvq_status lvq_copy_pages(const lvq_config* cfg, const lvq_layout* lay, int32_t n, const int32_t* pairs, uint8_t* idx,
+                          int32_t* dev_status, void* stream) {
+  Geo g;
+  lvq_status s = check_all(cfg, lay, &g);
+  if (s != LVQ_OK) return s;
+  if (n < 0) return LVQ_EINVAL;
+  if (n > 0 && (!pairs || ((uintptr_t)pairs & 7u) || !idx || !aligned16(idx))) return LVQ_EINVAL;
+  if (!g.pool) return LVQ_EUNSUPPORTED;
+  if ((s = check_device()) != LVQ_OK) return s;
+  return cuda_status(launch_copy_pages(g, n, pairs, idx, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+lvq_status lvq_compact_pages(const lvq_config* cfg, const lvq_layout* lay, int32_t n_moves, const int32_t* moves,
+                             const int32_t* new_id, int32_t* page_table, uint8_t* idx, int32_t* dev_status,
+                             void* stream) {
+  Geo g;
+  lvq_status s = check_all(cfg, lay, &g);
+  if (s != LVQ_OK) return s;
+  if (!g.pool) return LVQ_EUNSUPPORTED;
+  if (n_moves < 0 || !new_id || page_table != g.pt) return LVQ_EINVAL;
+  if (n_moves > 0 && (!moves || ((uintptr_t)moves & 7u) || !idx || !aligned16(idx))) return LVQ_EINVAL;
+  if ((s = check_device()) != LVQ_OK) return s;
+  const int n_sm = device_sms();
+  if (n_sm < 1) return LVQ_ECUDA;
+  return cuda_status(launch_compact_pages(g, n_moves, moves, new_id, page_table, idx, dev_status, n_sm,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+lvq_status lvq_fork_requests(const lvq_config* cfg, const lvq_layout* lay, int32_t parent, int32_t n_children,
+                             const int32_t* children, int32_t coded_tokens, const int32_t* tail_pages,
+                             int32_t* ctx_len, int32_t* coded_len, void* sink, void* ring, uint8_t* idx,
+                             int32_t* page_table, int32_t* dev_status, void* stream) {
+  Geo g;
+  lvq_status s = check_all(cfg, lay, &g);
+  if (s != LVQ_OK) return s;
+  if (parent < 0 || parent >= g.B || n_children < 0 || coded_tokens < 0 || coded_tokens > (int64_t)g.P * kPage ||
+      page_table != g.pt)
+    return LVQ_EINVAL;
+  if (n_children > kForkMax) return LVQ_EUNSUPPORTED;
+  if (n_children > 0) {
+    if (!children || !ctx_len || !coded_len || !ring || !idx || !aligned16(ring) || !aligned16(idx)) return LVQ_EINVAL;
+    if (g.S > 0 && (!sink || !aligned16(sink))) return LVQ_EINVAL;
+    const bool tails = g.pool && coded_tokens % kPage != 0;
+    if (tails != (tail_pages != nullptr)) return LVQ_EINVAL;
+    for (int32_t i = 0; i < n_children; ++i) {
+      if (children[i] < 0 || children[i] >= g.B || children[i] == parent) return LVQ_EINVAL;
+      if (tails && (tail_pages[i] < 0 || tail_pages[i] >= g.pool)) return LVQ_EINVAL;
+      for (int32_t j = 0; j < i; ++j)
+        if (children[j] == children[i] || (tails && tail_pages[j] == tail_pages[i])) return LVQ_EINVAL;
+    }
+  }
+  if ((s = check_device()) != LVQ_OK) return s;
+  return cuda_status(launch_fork(g, parent, n_children, children, coded_tokens, tail_pages, ctx_len, coded_len,
+                                 static_cast<__nv_bfloat16*>(sink), static_cast<__nv_bfloat16*>(ring), idx, page_table,
+                                 dev_status, static_cast<cudaStream_t>(stream)));
+}
 
 lvq_status lvq_debug_faults(int64_t wait_iters, int32_t fault_mask) {
   if (fault_mask & ~(kFaultDecodeDropChunk | kFaultKmeansDropTile)) return LVQ_EINVAL;

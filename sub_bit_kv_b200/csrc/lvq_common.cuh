@@ -191,4 +191,18 @@ cudaError_t launch_encode_tc(const Geo& g, int layer, int req, const __nv_bfloat
                              int kv_tokens, int tok_begin, int n_tok, int coded_offset,
                              const __nv_bfloat16* cb, uint8_t* idx, int32_t* st, cudaStream_t s);
 bool encode_supported(int G, int c);
+cudaError_t launch_copy_pages(const Geo& g, int n, const int32_t* pairs, uint8_t* idx, int32_t* st, cudaStream_t s);
+cudaError_t launch_compact_pages(const Geo& g, int n_moves, const int32_t* moves, const int32_t* new_id, int32_t* table,
+                                 uint8_t* idx, int32_t* st, int n_sm, cudaStream_t s);
+constexpr int kForkMax = 256;           // children one lvq_fork_requests call can take
+cudaError_t launch_fork(const Geo& g, int parent, int n, const int32_t* children, int coded, const int32_t* tails,
+                        int32_t* ctx_len, int32_t* coded_len, __nv_bfloat16* sink, __nv_bfloat16* ring, uint8_t* idx,
+                        int32_t* table, int32_t* st, cudaStream_t s);
+constexpr int kSharedMaxBatch = 512;    // requests one lvq_decode_attention_shared call can take
+cudaError_t launch_decode_shared(const Geo& g, int layer, int step, int batch, const __nv_bfloat16* q,
+                                 const int32_t* ctx_len, const int32_t* coded_len, int n_groups,
+                                 const int32_t* group_begin, const int32_t* group_tokens, const __nv_bfloat16* sink,
+                                 const __nv_bfloat16* ring, const uint8_t* idx, const __nv_bfloat16* cbp,
+                                 const float* rope, int num_splits, float* ws, float* out, float* lse, int32_t* st,
+                                 int n_sm, cudaStream_t s);
 }  // namespace lvq

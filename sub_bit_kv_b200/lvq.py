@@ -71,6 +71,16 @@ _SIGS = {
     "lvq_pool_alloc": [_P, _I32, ctypes.POINTER(_I32)],
     "lvq_pool_free": [_P, ctypes.POINTER(_I32), _I32],
     "lvq_pool_available": [_P],
+    "lvq_pool_share": [_P, ctypes.POINTER(_I32), _I32],
+    "lvq_pool_holders": [_P, _I32],
+    "lvq_pool_renumber": [_P, ctypes.POINTER(_I32)],
+    "lvq_plan_compaction": [_I32, _P, _I32, _P, _P, ctypes.POINTER(_I32)],
+    "lvq_copy_pages": [ctypes.POINTER(lvq_config), ctypes.POINTER(lvq_layout), _I32, _P, _P, _P, _P],
+    "lvq_compact_pages": [ctypes.POINTER(lvq_config), ctypes.POINTER(lvq_layout), _I32, _P, _P, _P, _P, _P, _P],
+    "lvq_fork_requests": [ctypes.POINTER(lvq_config), ctypes.POINTER(lvq_layout), _I32, _I32, ctypes.POINTER(_I32),
+                          _I32, ctypes.POINTER(_I32), _P, _P, _P, _P, _P, _P, _P, _P],
+    "lvq_decode_attention_shared": [ctypes.POINTER(lvq_config), ctypes.POINTER(lvq_layout), _I32, _I32, _I32, _P,
+                                    _P, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _P],
 }
 EXPORTED = tuple(_SIGS)
 
@@ -116,6 +126,7 @@ class PagePool:
         h = _P()
         _check(lib().lvq_pool_create(int(n_pages), ctypes.byref(h)), "lvq_pool_create")
         self._h = h
+        self.n_pages = int(n_pages)
 
     def alloc(self, n: int) -> list:
         ids = (_I32 * max(1, n))()
@@ -128,6 +139,23 @@ class PagePool:
 
     def available(self) -> int:
         return int(lib().lvq_pool_available(self._h))
+
+    def share(self, ids) -> None:
+        """One more holder of each page; each holder frees it once."""
+        arr = (_I32 * max(1, len(ids)))(*ids)
+        _check(lib().lvq_pool_share(self._h, arr, len(ids)), "lvq_pool_share")
+
+    def holders(self, page: int) -> int:
+        """Holders of a page (0: free, -1: no such page)."""
+        return int(lib().lvq_pool_holders(self._h, int(page)))
+
+    def renumber(self, new_id) -> None:
+        """The pages take the ids of a compaction plan (new_id[old], -1 for free pages)."""
+        new_id = torch.as_tensor(new_id, dtype=torch.int32, device="cpu").contiguous()
+        if new_id.numel() != self.n_pages:
+            raise ValueError(f"new_id holds {new_id.numel()} ids, the pool {self.n_pages} pages")
+        _check(lib().lvq_pool_renumber(self._h, ctypes.cast(new_id.data_ptr(), ctypes.POINTER(_I32))),
+               "lvq_pool_renumber")
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -272,6 +300,119 @@ def lvq_decode_attention_noalloc(cfg, lay, layer, step, batch, q, ctx_len, coded
         _ptr(dev_status, "dev_status", torch.int32, 4), _stream(stream)), "lvq_decode_attention_noalloc")
 
 
+def _on(dev: int, t: Optional[torch.Tensor], name: str, dtype, min_bytes: int, optional=False):
+    """_ptr for the calls below, which also refuse a tensor of another device than `dev`, the current one."""
+    p = _ptr(t, name, dtype, min_bytes, optional)
+    if p is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return p
+
+
+def _table(cfg, lay, dev: int, page_table):
+    if cfg.pool_pages > 0:
+        return _on(dev, page_table, "page_table", torch.int32, lay.page_table_bytes)
+    if page_table is not None:
+        raise ValueError("page_table belongs to pool mode")
+    return None
+
+
+def lvq_decode_attention_shared(cfg, lay, layer, step, batch, q, ctx_len, coded_len, group_begin, group_tokens, sink,
+                                ring, idx, cbp, rope, num_splits, workspace, out, lse, dev_status, stream=None):
+    """lvq_decode_attention for groups of requests whose first coded tokens are the same: group i holds
+    the requests group_begin[i] .. group_begin[i + 1] - 1 and shares group_tokens[i] coded tokens, which
+    are restored once for all of them.  group_begin: int32 [n_groups + 1], group_tokens: int32 [n_groups],
+    both on the device.  num_splits = 0: the library's choice."""
+    d, hq, dev = cfg.head_dim, cfg.n_q_heads, torch.cuda.current_device()
+    n_groups = 0 if group_tokens is None else group_tokens.numel()
+    _check(lib().lvq_decode_attention_shared(
+        ctypes.byref(cfg), ctypes.byref(lay), layer, step, batch,
+        _on(dev, q, "q", torch.bfloat16, 2 * batch * hq * d),
+        _on(dev, ctx_len, "ctx_len", torch.int32, 4 * batch), _on(dev, coded_len, "coded_len", torch.int32, 4 * batch),
+        n_groups, _on(dev, group_begin, "group_begin", torch.int32, 4 * (n_groups + 1)),
+        _on(dev, group_tokens, "group_tokens", torch.int32, 4 * n_groups),
+        _on(dev, sink, "sink", torch.bfloat16, lay.sink_bytes), _on(dev, ring, "ring", torch.bfloat16, lay.ring_bytes),
+        _on(dev, idx, "idx", torch.uint8, lay.idx_bytes), _on(dev, cbp, "cbp", torch.bfloat16, lay.cbp_bytes),
+        _on(dev, rope, "rope", torch.float32, lay.rope_bytes), num_splits,
+        _on(dev, workspace, "workspace", torch.float32, lay.workspace_bytes),
+        _on(dev, out, "out", torch.float32, 4 * batch * hq * d), _on(dev, lse, "lse", torch.float32, 4 * batch * hq),
+        _on(dev, dev_status, "dev_status", torch.int32, 4), _stream(stream)), "lvq_decode_attention_shared")
+
+
+def lvq_copy_pages(cfg, lay, pairs, idx, dev_status, stream=None):
+    """Copies pages of the pool in every (layer, block, head, K/V).  pairs: device int32 [n][2], (source,
+    destination); no destination twice, none that is also a source."""
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be [n][2]")
+    dev, n = torch.cuda.current_device(), pairs.shape[0]
+    _check(lib().lvq_copy_pages(
+        ctypes.byref(cfg), ctypes.byref(lay), n, _on(dev, pairs, "pairs", torch.int32, 0),
+        _on(dev, idx, "idx", torch.uint8, lay.idx_bytes), _on(dev, dev_status, "dev_status", torch.int32, 4),
+        _stream(stream)), "lvq_copy_pages")
+
+
+class CompactionPlan:
+    """What lvq_plan_compaction writes: new_id (host int32 [n_pages], -1: not live), n_live, and the
+    moves for lvq_compact_pages (host int32 [n_moves][2])."""
+
+    def __init__(self, n_pages: int, order):
+        order = torch.as_tensor(order, dtype=torch.int32, device="cpu").contiguous()
+        n = order.numel()
+        self.n_pages = int(n_pages)
+        # one buffer, so that it goes to the device in one copy: the moves, then new_id
+        self._room = 2 * (n + n // 2)
+        pin = torch.cuda.is_available()
+        self._host = torch.empty(self._room + max(1, self.n_pages), dtype=torch.int32, pin_memory=pin)
+        k = _I32()
+        base = self._host.data_ptr()
+        _check(lib().lvq_plan_compaction(self.n_pages, order.data_ptr() if n else None, n, base + 4 * self._room,
+                                         base if n else None, ctypes.byref(k)), "lvq_plan_compaction")
+        self.n_moves = k.value
+        self.moves = self._host[:2 * k.value].view(-1, 2)
+        self.new_id = self._host[self._room:]
+
+    @property
+    def n_live(self) -> int:
+        return int((self.new_id >= 0).sum())
+
+
+def lvq_plan_compaction(n_pages, order) -> CompactionPlan:
+    """Plans a compaction of a pool of n_pages pages: the pages in `order` (a list or a CPU tensor; a page
+    named again keeps its first place) get the ids 0, 1, ...; host work only."""
+    return CompactionPlan(n_pages, order)
+
+
+def lvq_compact_pages(cfg, lay, plan: CompactionPlan, page_table, idx, dev_status, stream=None):
+    """Carries out a compaction plan in place on the pool's codes and rewrites the page table."""
+    if plan.n_pages != cfg.pool_pages:
+        raise ValueError(f"the plan is for a pool of {plan.n_pages} pages, the configuration has {cfg.pool_pages}")
+    dev, raw = torch.cuda.current_device(), _stream(stream)
+    table, codes = _table(cfg, lay, dev, page_table), _on(dev, idx, "idx", torch.uint8, lay.idx_bytes)
+    status = _on(dev, dev_status, "dev_status", torch.int32, 4)
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=dev) if stream is not None else None):
+        plan_dev = plan._host.to(torch.device("cuda", dev), non_blocking=True)
+        _check(lib().lvq_compact_pages(
+            ctypes.byref(cfg), ctypes.byref(lay), plan.n_moves, plan_dev.data_ptr(),
+            plan_dev.data_ptr() + 4 * plan._room, table, codes, status, raw), "lvq_compact_pages")
+
+
+def lvq_fork_requests(cfg, lay, parent, children, coded_tokens, tail_pages, ctx_len, coded_len, sink, ring, idx,
+                      page_table, dev_status, stream=None):
+    """Makes every request of `children` (a list) a copy of `parent`, which has coded_tokens coded tokens.
+    tail_pages: in pool mode, where coded_tokens is not a multiple of 8, a page of its own for each child
+    (else None).  CodedCache.fork also does the pool's bookkeeping."""
+    dev, n = torch.cuda.current_device(), len(children)
+    if tail_pages is not None and len(tail_pages) != n:
+        raise ValueError(f"{len(tail_pages)} tail pages for {n} children")
+    b = 4 * cfg.max_batch
+    _check(lib().lvq_fork_requests(
+        ctypes.byref(cfg), ctypes.byref(lay), parent, n, (_I32 * max(1, n))(*children), coded_tokens,
+        None if tail_pages is None else (_I32 * max(1, n))(*tail_pages),
+        _on(dev, ctx_len, "ctx_len", torch.int32, b), _on(dev, coded_len, "coded_len", torch.int32, b),
+        _on(dev, sink, "sink", torch.bfloat16, lay.sink_bytes), _on(dev, ring, "ring", torch.bfloat16, lay.ring_bytes),
+        _on(dev, idx, "idx", torch.uint8, lay.idx_bytes), _table(cfg, lay, dev, page_table),
+        _on(dev, dev_status, "dev_status", torch.int32, 4), _stream(stream)), "lvq_fork_requests")
+
+
 def lvq_dequantize(cfg, lay, layer, step, req, kv, idx, cbp, tok_begin, n_tok, out, stream=None):
     _check(lib().lvq_dequantize(
         ctypes.byref(cfg), ctypes.byref(lay), layer, step, req, kv, _ptr(idx, "idx", torch.uint8, lay.idx_bytes),
@@ -325,6 +466,52 @@ class CodedCache:
             self.pool.free(self.pages[b])
             self.pages[b] = []
             self.page_table[b * self.lay.page_table_stride:(b + 1) * self.lay.page_table_stride].fill_(-1)
+
+    def fork(self, parent: int, children, coded_tokens: int, stream=None) -> None:
+        """Every request of `children` becomes a copy of request `parent`, which has coded_tokens coded
+        tokens.  In pool mode the children hold the parent's full pages with it and get a page of their
+        own for a partial last one; they must hold no pages before."""
+        children = list(children)
+        tails = None
+        if self.pool is not None:
+            if any(self.pages[c] for c in children):
+                raise ValueError("a child holds pages: release it first")
+            full, rest = divmod(coded_tokens, 8)
+            if len(self.pages[parent]) < full + (rest > 0):
+                raise ValueError(f"request {parent} holds {len(self.pages[parent])} pages, {coded_tokens} coded tokens need more")
+            if rest:
+                tails = self.pool.alloc(len(children))
+        try:
+            lvq_fork_requests(self.cfg, self.lay, parent, children, coded_tokens, tails, self.ctx_len, self.coded_len,
+                              self.sink, self.ring, self.idx, getattr(self, "page_table", None), self.status, stream)
+        except Exception:
+            if tails:
+                self.pool.free(tails)
+            raise
+        if self.pool is not None:
+            for i, c in enumerate(children):
+                self.pool.share(self.pages[parent][:full])
+                self.pages[c] = self.pages[parent][:full] + ([tails[i]] if tails else [])
+
+    def compact(self, stream=None) -> int:
+        """Pool mode: the pages in use move to the lowest ids, each request's pages next to one another
+        (a shared page with the first request that holds it), so that its reads form long runs.
+        Returns the number of pages moved."""
+        if self.pool is None:
+            raise ValueError("compaction belongs to pool mode")
+        plan = lvq_plan_compaction(self.cfg.pool_pages, [p for row in self.pages for p in row])
+        self.pool.renumber(plan.new_id)         # refuses pages that are held outside the requests' lists
+        try:
+            lvq_compact_pages(self.cfg, self.lay, plan, self.page_table, self.idx, self.status, stream)
+        except Exception:
+            old = torch.full_like(plan.new_id, -1)
+            live = plan.new_id >= 0
+            old[plan.new_id[live].long()] = torch.arange(old.numel(), dtype=torch.int32)[live]
+            self.pool.renumber(old)
+            raise
+        to = plan.new_id.tolist()
+        self.pages = [[to[p] for p in row] for row in self.pages]
+        return plan.n_moves
 
     # shaped views of the caller-owned buffers (layouts from lvq_cache_layout)
     def cb_view(self):
