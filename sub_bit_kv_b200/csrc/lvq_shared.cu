@@ -7,13 +7,15 @@
 // scored against every query of the group.
 //
 // Work.  A KV head's work is a list of entries: for every group its shared tokens, once per tile of
-// kQT query rows (request, query head of the KV head); then for every request its own tokens (sink,
-// the rest of its coded tokens, recent window), once per tile of its query heads.  An entry costs
+// 16 query rows (request, query head of the KV head); then for every request its own tokens (the
+// rest of its coded ones, sink and recent window), once per 8 of its query heads.  An entry costs
 // its 16-token tiles and a fixed overhead per query tile; the list is cut into k parts of equal
 // cost, and CTA (j, h) takes part j of KV head h.  Every CTA derives the same cut from the
-// counters.  Per entry it covers, a CTA leaves one partial (m, l, o) per query row; every row has a
-// slot per part and kind (shared, own), and the merge kernel joins the ones that are not empty in
-// a fixed order.
+// counters.  All 8 warps of a CTA work on one shared entry at a time; the own entries of a part
+// are cut once more, a contiguous run of tiles to a warp, so that the latencies of 8 small entries
+// overlap.  Per entry it covers, a CTA leaves one partial (m, l, o) per query row; every row has a
+// slot per part and kind (shared, own), and the merge kernel joins the ones that are not empty.
+// Every sum is taken in a fixed order.
 #include <cuda_fp16.h>
 
 #include "lvq_common.cuh"
@@ -22,11 +24,14 @@ namespace lvq {
 
 namespace {
 
-constexpr int kQT = 16;                 // query rows of a tile
-constexpr int kTT = 16;                 // tokens of a tile
-constexpr int kOverhead = 20;           // fixed cost of an entry's query tile, in token tiles
+constexpr int kQT = 16;                 // query rows of a tile of shared tokens
+constexpr int kOT = 8;                  // query heads of a tile of own tokens
+constexpr int kTT = 16;                 // tokens of a tile: two pages
+constexpr int kSharedCost = 20;         // fixed cost of a query tile of a shared entry, in token tiles
+constexpr int kOwnCost = 3;             // the same of an own entry
 constexpr int kWarps = 8;
 constexpr int kShThreads = 32 * kWarps;
+constexpr float kNoMax = -1e30f;        // softmax reference before the first token
 
 struct SharedArgs {
   int layer, step, batch, ng, k;
@@ -51,15 +56,46 @@ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Entries 0 .. ng-1: the groups' shared tokens; ng .. ng+batch-1: the requests' own tokens.
 struct Entry {
-  int tiles, qtiles;                    // token tiles, query tiles
-  __device__ long long cost() const { return tiles ? (long long)qtiles * (kOverhead + tiles) : 0; }
+  int tiles, qtiles, fixed;             // token tiles, query tiles, fixed cost of a query tile
+  __device__ long long each() const { return fixed + tiles; }
+  __device__ long long cost() const { return tiles ? qtiles * each() : 0; }
 };
 __device__ inline Entry entry_of(const Geo& g, const Counters& c, int ng, int e) {
   const int rep = g.Hq / g.H;
-  if (e < ng) return {c.sh[e] / kTT + (c.sh[e] % kTT != 0), ceil_div((c.gb[e + 1] - c.gb[e]) * rep, kQT)};
-  const int b = e - ng, ctx = c.ctx[b];
-  const int S_eff = min(g.S, ctx), recent = ctx - S_eff - c.coded[b];
-  return {ceil_div(S_eff, kTT) + ceil_div(c.coded[b] - c.own0[b], kTT) + ceil_div(recent, kTT), ceil_div(rep, kQT)};
+  if (e < ng) return {ceil_div(c.sh[e], kTT), ceil_div((c.gb[e + 1] - c.gb[e]) * rep, kQT), kSharedCost};
+  const int b = e - ng, ctx = c.ctx[b], rest = c.coded[b] - c.own0[b];
+  return {ceil_div(rest, kTT) + ceil_div(ctx - c.coded[b], kTT), ceil_div(rep, kOT), kOwnCost};
+}
+
+// The entry of [e0, e1) in which cost `x` lies (counted from e0's start) and the cost before it; one
+// warp, the entries summed lane by lane.  e1 if x is not below the total, which *total receives.
+__device__ inline int locate(const Geo& g, const Counters& c, int ng, int e0, int e1, long long x, long long* before,
+                             long long* total) {
+  const int lane = threadIdx.x & 31, per = ceil_div(e1 - e0, 32);
+  long long mine = 0;
+  for (int i = lane * per; i < min(e1 - e0, (lane + 1) * per); ++i) mine += entry_of(g, c, ng, e0 + i).cost();
+  long long up = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += v;
+  }
+  *total = __shfl_sync(0xffffffffu, up, 31);
+  const unsigned in = __ballot_sync(0xffffffffu, up > x);
+  if (in == 0) {
+    *before = *total;
+    return e1;
+  }
+  const int first = __ffs(in) - 1;
+  long long at = __shfl_sync(0xffffffffu, up - mine, first);
+  int e = e0 + first * per;
+  for (;; ++e) {
+    const long long cost = entry_of(g, c, ng, e).cost();
+    if (at + cost > x) break;
+    at += cost;
+  }
+  *before = at;
+  return e;
 }
 
 // Loads and checks the counters; returns false (for every thread) if group_begin is not as described.
@@ -67,17 +103,17 @@ __device__ bool load_counters(const Geo& g, const SharedArgs& a, Counters& c, bo
   const int tid = threadIdx.x;
   bool ok = true;
   for (int i = tid; i <= a.ng; i += kShThreads) {
-    const int v = __ldg(a.gb + i);
+    const int v = __ldcg(a.gb + i);
     c.gb[i] = v;
     ok = ok && v >= 0 && v <= a.batch && (i > 0 || v == 0) && (i < a.ng || v == a.batch);
     if (i < a.ng) {
-      ok = ok && __ldg(a.gb + i + 1) >= v;
-      c.sh[i] = max(0, __ldg(a.gt + i)) / kPage * kPage;
+      ok = ok && __ldcg(a.gb + i + 1) >= v;
+      c.sh[i] = max(0, __ldcg(a.gt + i)) / kPage * kPage;
       c.lead[i] = a.batch;
     }
   }
   for (int b = tid; b < a.batch; b += kShThreads) {
-    const int ctx = __ldg(a.ctx_len + b), L = __ldg(a.coded_len + b);
+    const int ctx = __ldcg(a.ctx_len + b), L = __ldcg(a.coded_len + b);
     const int recent = ctx - min(g.S, max(ctx, 0)) - L;
     const bool bad = ctx < 1 || ctx > g.max_ctx || L < 0 || L > g.P * kPage || (L > 0 && ctx < g.S + L) || recent < 0 ||
                      recent > g.R;
@@ -143,23 +179,26 @@ struct Sh {
   static constexpr int KS = kEntries * D * 2;      // a step slice
   static constexpr int VROW = D * 2 + 16;          // a padded row of the value slice
   static constexpr int OROW = D + 4;               // a padded row of a warp's output, in floats
-  static constexpr int WARP = kQT * OROW * 4;      // a warp's area: code stages or bf16 rows, then its output
-  static constexpr int NST = WARP / STAGE < 6 ? WARP / STAGE : 6;
+  // a warp's area: code stages, a query tile's fragments or 8 output rows, then 8 output rows parked
+  // (a shared entry's 16 output rows take both)
+  static constexpr int WARP = kQT * OROW * 4;
+  static constexpr int PARK = kOT * OROW * 4;
+  static constexpr int NST = PARK / STAGE < 6 ? PARK / STAGE : 6;
   static constexpr int OFF_V = KS;
   static constexpr int OFF_W = OFF_V + kEntries * VROW;
-  static constexpr int OFF_Q = OFF_W + kWarps * WARP;
-  static constexpr int OFF_F = OFF_Q + 2 * NW * 32 * 16;
-  static constexpr int OFF_ML = OFF_F + NW * 32 * 16;
+  static constexpr int OFF_F = OFF_W + kWarps * WARP;
+  static constexpr int OFF_R = OFF_F + NW * 32 * 16;
+  static constexpr int OFF_ML = OFF_R + kWarps * F * 8;
   static constexpr int OFF_INV = OFF_ML + kWarps * kQT * 8;
   static constexpr int OFF_RED = OFF_INV + kQT * 4;
-  static constexpr int OFF_BAR = OFF_RED + 2 * kWarps * 4;
-  static constexpr int OFF_CUT = OFF_BAR + 16;
-  static constexpr int OFF_C = OFF_CUT + 32;
+  static constexpr int OFF_BAR = OFF_RED + 4 * kWarps * 4;
+  static constexpr int OFF_C = OFF_BAR + 16;
   static constexpr int smem(int batch, int ng) { return OFF_C + (3 * batch + 3 * ng + 1) * 4; }
   static_assert(NP % 4 == 0 && NI * C == 2 * NW, "lane mapping");
-  static_assert(NST >= 3 && kWarps * WARP >= KS && WARP >= 2 * kTT * D * 2, "the warps' areas");
+  static_assert(NST >= 3 && NST <= 8, "stages (a tile's RoPE row is read before the one 8 tiles on is fetched)");
+  static_assert(kWarps * WARP >= KS && WARP >= 2 * NW * 32 * 16 && PARK >= NW * 32 * 16, "the warps' areas");
   static_assert(OFF_C + (6 * kSharedMaxBatch + 1) * 4 <= 227 * 1024, "shared memory");
-  static_assert(OFF_W % 16 == 0 && OFF_BAR % 8 == 0 && OFF_CUT % 8 == 0, "alignment");
+  static_assert(OFF_W % 16 == 0 && PARK % 16 == 0 && OFF_F % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 };
 
 __device__ inline uint32_t pack_h2(float lo, float hi) {
@@ -167,30 +206,23 @@ __device__ inline uint32_t pack_h2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ inline uint32_t pack_b2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ inline float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 // a pair of values as the sum of two fp16 pairs: hi + lo, good to 2^-22 of each value (2^-25 at least)
 __device__ inline void split_h2(float2 v, uint32_t& hi, uint32_t& lo) {
   hi = pack_h2(v.x, v.y);
   const float2 b = unpack_h2(hi);
-  const float2 r = __fadd2_rn(v, make_float2(-b.x, -b.y));
-  lo = pack_h2(r.x, r.y);
+  lo = pack_h2(v.x - b.x, v.y - b.y);
 }
-__device__ inline float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+__device__ inline float2 b2_lohi(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
 __device__ inline void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ inline void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ inline void ldmatrix4_trans(uint32_t (&v)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
 __device__ inline float ex2(float x) {
   float y;
@@ -203,99 +235,430 @@ __device__ inline void cp_async16(uint32_t dst, const void* src) {
 __device__ inline void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ inline void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+__device__ inline void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(src), "r"(bytes) : "memory");
+}
+__device__ inline void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ inline void dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // 2^e as a float, e clamped to the normal range
 __device__ inline float pow2i(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
-// the largest finite magnitude of a bf16 pair, as the bits of a bf16 (infinities and NaN count nothing)
-__device__ inline uint32_t amax_b2(uint32_t w, uint32_t m) {
-  const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
-  m = max(m, lo < 0x7f80u ? lo : 0u);
-  return max(m, hi < 0x7f80u ? hi : 0u);
-}
 // the power of two that brings magnitudes up to that bf16 below 2^14 (none where all are zero; its reciprocal
 // and its products with weights up to 2^14 stay normal floats)
 __device__ inline int fit_exp(uint32_t bits) { return bits ? min(13 - ((int)(bits >> 7) - 127), 90) : 0; }
+__device__ inline int fit_exp_f(float m) { return m > 0.f && m < INFINITY ? min(13 - (((__float_as_int(m) >> 23) & 255) - 127), 90) : 0; }
 
-// A warp's running softmax over its tokens, for the 16 rows of the query tile: lane (r, quad) holds rows
-// r and r + 8.  m is a reference no more than 2^14 below the largest weight: p = 2^(s - m).
+// Channel of output tile i, fragment column n: the order in which the value fragments are restored.
+template <int D, int C>
+__device__ inline int out_channel(int i, int n) { return C == 4 ? n * (D / 8) + i : 8 * i + n; }
+
+// A warp's running softmax over its tokens: m is a reference no more than 2^14 below the largest weight,
+// p = 2^(s - m).  Shared entries: lane (r, quad) holds rows r and r + 8.  Own entries (stacked): rows 0-7
+// are the query heads with the operands' high parts, rows 8-15 the same with the low ones, so lane (r, quad)
+// holds both halves of row r, and only m[0], l[0] are used.
 template <int D, int C>
 struct State {
   float o[Sh<D, C>::NT][4];
   float m[2], l[2];
+  __device__ void clear() {
+#pragma unroll
+    for (int i = 0; i < Sh<D, C>::NT; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+    m[0] = m[1] = kNoMax;
+    l[0] = l[1] = 0.f;
+  }
 };
 
-// Scores of a token tile -> weights (and their sums); the outputs are rescaled only when a row's largest
-// score outgrows its reference by 2^14, so that weights stay within fp16.
+// What the restoration of coded tokens needs, per CTA and lane.
 template <int D, int C>
-__device__ inline void softmax_tile(State<D, C>& st, float (&s)[2][4], const float (&inv)[2], int n, int quad) {
-  if (n < kTT) {
+struct Book {
+  const unsigned char *Ks, *Vs;         // step slices: keys bf16, values scaled fp16 in padded rows
+  const float4* Ff;                     // [frequency pair][lane]: (cos, cos, sin, sin) at (S % 8 + j)
+  float2 ec[Sh<D, C>::NW], es[Sh<D, C>::NW];   // the lane's e^{i 8 theta}
+  float ks, kinv;                       // key scale (a power of two) and its reciprocal
+};
+
+// A run of coded tokens of one request (or of a group's first): logical pages [pg0, pg_end), n tokens.
+struct Run {
+  int lead, pg0, pg_end, n;
+  const uint8_t *kcode, *vcode;         // code streams (pool mode: pools) of the head
+};
+
+// Restores the run's tokens tile by tile and adds them to the state.  STK: stacked rows.  Per tile, lane
+// (j, quad) restores token j of each of the two pages: the entries of pair-groups P = quad + 4 i straight
+// into the B fragments of mma.sync m16n8k16 (the order of a dot product's channels is free, so a fragment's k
+// indices are the channels of the lane's own entries), rotated in fp32 by e^{i p theta}, which moves on by a
+// page (8 positions) with one complex multiplication and is taken anew from the tables every 16 pages.  Keys
+// and queries enter as sums of two fp16 values, good to 2^-22 of the largest; lo x lo is left out of 16 rows.
+// Weights too are sums of two fp16 values; values are exact.
+template <int D, int C, bool STK>
+__device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, const Book<D, C>& bk, const Run& run, State<D, C>& st,
+                                          const uint32_t (&qf)[STK ? 1 : 2][Sh<D, C>::NW][4], const float (&qinv)[2],
+                                          unsigned char* stages, float4* rrow) {
+  using X = Sh<D, C>;
+  const int lane = threadIdx.x & 31, quad = lane & 3, row = lane >> 2;
+  const int nt = ceil_div(run.n, kTT);
+  const float4* rope4 = reinterpret_cast<const float4*>(a.rope);     // two frequencies: (cos, sin, cos, sin)
+  const uint32_t stage0 = smem_addr(stages), vs0 = smem_addr(bk.Vs);
+  const float inv[2] = {qinv[0] * bk.kinv, qinv[1] * bk.kinv};
+  int ids = 0, ids_at = -32;                                         // physical pages [ids_at, ids_at + 32) of the run
+  auto fetch = [&](int t) {                                          // tile t's codes into its stage
+    const int pp = 2 * t;
+    if (pp - ids_at >= 32) {
+      ids_at = pp;
+      ids = phys_page(g, run.lead, min(run.pg0 + pp + lane, run.pg_end - 1));
+      if (ids < 0) {
+        set_status(a.st, LVQ_ECAPACITY);
+        ids = 0;
+      }
+    }
+    const int i0 = __shfl_sync(0xffffffffu, ids, pp - ids_at), i1 = __shfl_sync(0xffffffffu, ids, pp + 1 - ids_at);
+    const uint32_t dst = stage0 + (t % X::NST) * X::STAGE;
+    constexpr int VP = X::PAGE / 16;
+#pragma unroll
+    for (int v = lane; v < 4 * VP; v += 32) {
+      const int id = (v / VP) & 1 ? i1 : i0;
+      cp_async16(dst + v * 16, (v < 2 * VP ? run.kcode : run.vcode) + (size_t)id * X::PAGE + v % VP * 16);
+    }
+    if (t % 8 == 0 && lane < X::F / 2)                               // the RoPE row of its first page
+      cp_async16(smem_addr(rrow) + lane * 16, rope4 + (size_t)(run.pg0 + pp + (g.S >> 3)) * (X::F / 2) + lane);
+  };
+#pragma unroll
+  for (int t = 0; t < X::NST - 1; ++t) {
+    if (t < nt) fetch(t);
+    cp_commit();
+  }
+  float2 wc[X::NW], ws[X::NW];
+  for (int t = 0; t < nt; ++t) {
+    cp_wait<X::NST - 2>();
+    __syncwarp();
+    if (t % 8 == 0) {
+#pragma unroll
+      for (int w = 0; w < X::NW; ++w) {
+        const float4 x = rrow[((quad + 4 * (w / (C / 2))) * C + 2 * (w % (C / 2))) / 2], y = bk.Ff[w * 32 + lane];
+        wc[w] = make_float2((x.x * y.x - x.y * y.z) * bk.ks, (x.z * y.y - x.w * y.w) * bk.ks);
+        ws[w] = make_float2((x.x * y.z + x.y * y.x) * bk.ks, (x.z * y.w + x.w * y.y) * bk.ks);
+      }
+    }
+    const unsigned char* codes = stages + (t % X::NST) * X::STAGE;
+    float sh[2][4] = {}, sl[2][4] = {};                              // products of the high parts, and the others
+#pragma unroll
+    for (int i = 0; i < X::NI; ++i) {
+      const int P = quad + 4 * i;
+      const unsigned char *e0[2], *e1[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t k0 = codes[u * X::PAGE + P * kPage + row], k1 = codes[u * X::PAGE + (P + X::NP) * kPage + row];
+        e0[u] = bk.Ks + k0 * (2 * D) + P * (2 * C);
+        e1[u] = bk.Ks + k1 * (2 * D) + (P + X::NP) * (2 * C);
+      }
+#pragma unroll
+      for (int q = 0; q < (C + 7) / 8; ++q) {
+        uint32_t lo[2][4], hi[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if constexpr (C == 4) {
+            const uint2 x = *reinterpret_cast<const uint2*>(e0[u]), y = *reinterpret_cast<const uint2*>(e1[u]);
+            lo[u][0] = x.x; lo[u][1] = x.y; hi[u][0] = y.x; hi[u][1] = y.y;
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(e0[u] + 16 * q), y = *reinterpret_cast<const uint4*>(e1[u] + 16 * q);
+            lo[u][0] = x.x; lo[u][1] = x.y; lo[u][2] = x.z; lo[u][3] = x.w;
+            hi[u][0] = y.x; hi[u][1] = y.y; hi[u][2] = y.z; hi[u][3] = y.w;
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < (C < 8 ? C / 2 : 4); ++v) {
+          const int w = i * (C / 2) + q * 4 + v;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float2 x = b2_lohi(lo[u][v]), y = b2_lohi(hi[u][v]), c = wc[w], s = ws[w];
+            // (scalar where a sign changes: packed operands have none to spare)
+            const float2 r = make_float2(x.x * c.x - y.x * s.x, x.y * c.y - y.y * s.y);
+            const float2 z = __ffma2_rn(y, c, __fmul2_rn(x, s));
+            uint32_t rh, rl, zh, zl;
+            split_h2(r, rh, rl);
+            split_h2(z, zh, zl);
+            mma_f16(sl[u], qf[0][w], rl, zl);
+            if constexpr (!STK) mma_f16(sl[u], qf[STK ? 0 : 1][w], rh, zh);
+            mma_f16(sh[u], qf[0][w], rh, zh);
+            wc[w] = make_float2(c.x * bk.ec[w].x - s.x * bk.es[w].x, c.y * bk.ec[w].y - s.y * bk.es[w].y);
+            ws[w] = __ffma2_rn(s, bk.ec[w], __fmul2_rn(c, bk.es[w]));
+          }
+        }
+      }
+    }
+    // ---- scores -> weights: column 2 quad + k of page u; masked past the run's last token
+    constexpr int NR = STK ? 1 : 2;
+    const int n = min(kTT, run.n - t * kTT);
+    float s[NR][2][2];                                               // [row][page][k]
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v = sh[u][2 * r + k] + sl[u][2 * r + k];
+          if constexpr (STK) v += sh[u][2 + k] + sl[u][2 + k];
+          s[r][u][k] = v * inv[r];
+        }
+    if (n < kTT) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (8 * u + 2 * quad + k >= n)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) s[r][u][k] = -INFINITY;
+    }
+    float top[NR];
+    bool grow = false;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      top[r] = fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][1][0], s[r][1][1]));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+      grow = grow || top[r] > st.m[r] + 14.f;
+    }
+    // outputs are rescaled only when a row outgrows its reference by 2^14, so that weights stay within fp16
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float mn = top[r] > st.m[r] + 14.f ? top[r] - 6.f : st.m[r];
+        const float al = ex2(st.m[r] - mn);
+        st.m[r] = mn;
+        st.l[r] *= al;
+#pragma unroll
+        for (int i = 0; i < X::NT; ++i)
+#pragma unroll
+          for (int k = 0; k < (STK ? 4 : 2); ++k) st.o[i][2 * r + k] *= al;
+      }
+    }
+    uint32_t ph[4], pl[4];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[u][k] = 8 * u + 2 * quad + (k & 1) < n ? s[u][k] * inv[k >> 1] : -INFINITY;
-  } else {
+      for (int r = 0; r < NR; ++r) {
+        const float2 p = make_float2(ex2(s[r][u][0] - st.m[r]), ex2(s[r][u][1] - st.m[r]));
+        st.l[r] += p.x + p.y;
+        if constexpr (STK) split_h2(p, ph[2 * u], ph[2 * u + 1]);
+        else split_h2(p, ph[2 * u + r], pl[2 * u + r]);
+      }
+    // ---- values.  Masked tokens take the tile's first token instead: nothing else is read
+    const unsigned char* vcodes = codes + 2 * X::PAGE;
+    if constexpr (C >= 8) {
+      // ldmatrix hands out 8 tokens x 8 channels transposed: lane l names token l % 16, unit 2 i + l / 16
+      const int tok = (lane & 15) < n ? lane & 15 : 0;
+      const unsigned char* vc = vcodes + (tok >> 3) * X::PAGE + (tok & 7);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+      for (int i = 0; i < X::NT / 2; ++i) {
+        const int unit = 2 * i + (lane >> 4);
+        const uint32_t code = vc[unit * 8 / C * kPage];
+        uint32_t v[4];
+        ldmatrix4_trans(v, vs0 + code * X::VROW + unit * 16);
+        if constexpr (!STK) {
+          mma_f16(st.o[2 * i], pl, v[0], v[1]);
+          mma_f16(st.o[2 * i + 1], pl, v[2], v[3]);
+        }
+        mma_f16(st.o[2 * i], ph, v[0], v[1]);
+        mma_f16(st.o[2 * i + 1], ph, v[2], v[3]);
+      }
+    } else {
+      // entries of 4 channels: lane (n, quad) takes channels [n d/8, (n + 1) d/8) of tokens 2 quad, 2 quad + 1 of
+      // both pages and pairs the tokens up
+      const int t0 = 2 * quad < n ? 2 * quad : 0, t1 = 2 * quad + 1 < n ? 2 * quad + 1 : 0;
+      const int t2 = 8 + 2 * quad < n ? 8 + 2 * quad : 0, t3 = 9 + 2 * quad < n ? 9 + 2 * quad : 0;
+      const int toks[4] = {t0, t1, t2, t3};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[u][k] *= inv[k >> 1];
+      for (int q = 0; q < D / 32; ++q) {                             // 4 channels: one entry of each token
+        const int grp = row * (D / 32) + q;
+        uint2 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t code = vcodes[(toks[k] >> 3) * X::PAGE + grp * kPage + (toks[k] & 7)];
+          v[k] = *reinterpret_cast<const uint2*>(bk.Vs + code * X::VROW + grp * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t sel = i & 1 ? 0x7632u : 0x5410u;
+          const uint32_t b0 = i < 2 ? __byte_perm(v[0].x, v[1].x, sel) : __byte_perm(v[0].y, v[1].y, sel);
+          const uint32_t b1 = i < 2 ? __byte_perm(v[2].x, v[3].x, sel) : __byte_perm(v[2].y, v[3].y, sel);
+          if constexpr (!STK) mma_f16(st.o[4 * q + i], pl, b0, b1);
+          mma_f16(st.o[4 * q + i], ph, b0, b1);
+        }
+      }
+    }
+    __syncwarp();                                                    // the stage is read
+    if (t + X::NST - 1 < nt) fetch(t + X::NST - 1);
+    cp_commit();
   }
-  float t[2];
+  cp_wait<0>();
+  __syncwarp();
+}
+
+// The bf16 tokens [i0, i1) of request b's list (sink tokens, then recent ones) against NR query heads, on
+// CUDA cores: D / 4 lanes to a token, a lane two frequencies (channels 2 f, 2 f + 1 and their partners) of
+// the key and four channels of the value; the rotation moves on by a token at a time.  Eight tokens (16 at
+// d = 64) are loaded at once.  Row r's outputs are joined with what its area row holds (`fresh`: nothing yet).
+template <int D, int C, int NR>
+__device__ __forceinline__ void bf16_run(const Geo& g, const SharedArgs& a, const Counters& c, int b, int h, const __nv_bfloat16* q,
+                                         float scale, int i0, int i1, float* area, float2* ml, bool fresh) {
+  using X = Sh<D, C>;
+  constexpr int LPT = D / 4, TPW = 32 / LPT, NB = 8;
+  const int lane = threadIdx.x & 31, fp = lane % LPT, half = lane / LPT;
+  const float4* rope4 = reinterpret_cast<const float4*>(a.rope);
+  auto angle = [&](int p) {                                          // (cos, cos, sin, sin) at position p
+    const float4 x = __ldg(rope4 + (size_t)(p >> 3) * (X::F / 2) + fp), y = __ldg(rope4 + (size_t)(g.RC + (p & 7)) * (X::F / 2) + fp);
+    return make_float4(x.x * y.x - x.y * y.y, x.z * y.z - x.w * y.w, x.x * y.y + x.y * y.x, x.z * y.w + x.w * y.z);
+  };
+  const int ctx = c.ctx[b], coded = c.coded[b], S_eff = min(g.S, ctx);
+  float4 z[NR];                                                      // rotated queries: channels f, f + 1, f + d/2, f + 1 + d/2
+  const float4 wq = angle(ctx - 1);
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    t[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-    t[r] = fmaxf(t[r], __shfl_xor_sync(0xffffffffu, t[r], 1));
-    t[r] = fmaxf(t[r], __shfl_xor_sync(0xffffffffu, t[r], 2));
+  for (int r = 0; r < NR; ++r) {
+    const uint32_t* qr = reinterpret_cast<const uint32_t*>(q + (size_t)r * D);
+    const float2 x = b2_lohi(__ldg(qr + fp)), y = b2_lohi(__ldg(qr + fp + X::F / 2));
+    z[r] = make_float4((x.x * wq.x - y.x * wq.z) * scale, (x.y * wq.y - y.y * wq.w) * scale, (y.x * wq.x + x.x * wq.z) * scale,
+                       (y.y * wq.y + x.y * wq.w) * scale);
   }
-  if (__any_sync(0xffffffffu, t[0] > st.m[0] + 14.f || t[1] > st.m[1] + 14.f)) {
+  const float4 dw = angle(TPW);
+  float m[NR], l[NR], o[NR][4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float mn = t[r] > st.m[r] + 14.f ? t[r] - 6.f : st.m[r];
-      const float al = ex2(st.m[r] - mn);
-      st.m[r] = mn;
-      st.l[r] *= al;
+  for (int r = 0; r < NR; ++r) {
+    m[r] = kNoMax;
+    l[r] = o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
+  }
+#pragma unroll 1
+  for (int src = 0; src < 2; ++src) {
+    const int ra = src == 0 ? i0 : max(i0, S_eff), rb = src == 0 ? min(i1, S_eff) : i1;
+    if (ra >= rb) continue;
+    const __nv_bfloat16* kb = src == 0 ? a.sink + sink_off(g, a.layer, 0, a.step, b, h, 0) : a.ring + ring_off(g, a.layer, 0, a.step, b, h, 0);
+    const __nv_bfloat16* vb = src == 0 ? a.sink + sink_off(g, a.layer, 1, a.step, b, h, 0) : a.ring + ring_off(g, a.layer, 1, a.step, b, h, 0);
+    const int p0 = src == 0 ? ra : g.S + coded + ra - S_eff;
+    int slot = src == 0 ? ra + half : (coded + ra - S_eff + half) % g.R;
+    // (lanes of a token past the last one may start past it: their position only has to lie within the tables)
+    float4 w = angle(min(p0 + half, g.max_ctx - 1));
+#pragma unroll 1
+    for (int t0 = ra; t0 < rb; t0 += NB * TPW) {
+      uint32_t kx[NB], ky[NB];
+      uint2 vv[NB];
 #pragma unroll
-      for (int i = 0; i < Sh<D, C>::NT; ++i) { st.o[i][2 * r] *= al; st.o[i][2 * r + 1] *= al; }
+      for (int u = 0; u < NB; ++u) {
+        kx[u] = ky[u] = 0u;
+        vv[u] = make_uint2(0u, 0u);
+        if (t0 + u * TPW + half < rb) {
+          const uint32_t* kr = reinterpret_cast<const uint32_t*>(kb + (size_t)slot * D);
+          kx[u] = __ldg(kr + fp);
+          ky[u] = __ldg(kr + fp + X::F / 2);
+          vv[u] = __ldg(reinterpret_cast<const uint2*>(vb + (size_t)slot * D) + fp);
+        }
+        slot += TPW;
+        if (src == 1 && slot >= g.R) slot -= g.R;                     // (TPW <= R)
+      }
+      float d[NR][NB];
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        const float2 x = b2_lohi(kx[u]), y = b2_lohi(ky[u]);
+        const float k0 = x.x * w.x - y.x * w.z, k1 = x.y * w.y - y.y * w.w, k2 = y.x * w.x + x.x * w.z, k3 = y.y * w.y + x.y * w.w;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) d[r][u] = z[r].x * k0 + z[r].y * k1 + (z[r].z * k2 + z[r].w * k3);
+        w = make_float4(w.x * dw.x - w.z * dw.z, w.y * dw.y - w.w * dw.w, w.z * dw.x + w.x * dw.z, w.w * dw.y + w.y * dw.w);
+      }
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        // lane sums, transposed: lane keeps token tk = bits (4 2 1 of fp's low bits) of its token group
+#pragma unroll
+        for (int hb = NB / 2; hb > 0; hb >>= 1) {
+          const bool up = (fp & hb) != 0;
+#pragma unroll
+          for (int k = 0; k < hb; ++k) {
+            const float send = up ? d[r][k] : d[r][k + hb], keep = up ? d[r][k + hb] : d[r][k];
+            d[r][k] = keep + __shfl_xor_sync(0xffffffffu, send, hb);
+          }
+        }
+        float s = d[r][0];
+#pragma unroll
+        for (int o2 = NB; o2 < LPT; o2 <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o2);
+        const int tk = fp & (NB - 1);
+        if (t0 + tk * TPW + half >= rb) s = -INFINITY;
+        float top = s;
+#pragma unroll
+        for (int o2 = 1; o2 < NB; o2 <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+        if (TPW == 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const float mn = fmaxf(m[r], top), al = ex2(m[r] - mn), p = ex2(s - mn);
+        m[r] = mn;
+        l[r] = l[r] * al + (fp < NB ? p : 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[r][k] *= al;
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+          const float pu = __shfl_sync(0xffffffffu, p, u + half * LPT);
+          const float2 v0 = b2_lohi(vv[u].x), v1 = b2_lohi(vv[u].y);
+          o[r][0] = fmaf(pu, v0.x, o[r][0]);
+          o[r][1] = fmaf(pu, v0.y, o[r][1]);
+          o[r][2] = fmaf(pu, v1.x, o[r][2]);
+          o[r][3] = fmaf(pu, v1.y, o[r][3]);
+        }
+      }
     }
   }
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int r = 0; r < NR; ++r) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      s[u][k] = ex2(s[u][k] - st.m[k >> 1]);
-      st.l[k >> 1] += s[u][k];
+    for (int o2 = 16; o2 > 0; o2 >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o2);
+    if (TPW == 2)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[r][k] += __shfl_xor_sync(0xffffffffu, o[r][k], 16);
+    float4* to = reinterpret_cast<float4*>(area + r * X::OROW) + fp;
+    if (fresh) {
+      if (half == 0) *to = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+      if (lane == 0) ml[r] = make_float2(m[r], l[r]);
+    } else {
+      const float2 x = ml[r];
+      const float M = fmaxf(m[r], x.x), f0 = ex2(x.x - M), f1 = ex2(m[r] - M);
+      __syncwarp();
+      if (half == 0) {
+        const float4 y = *to;
+        *to = make_float4(y.x * f0 + o[r][0] * f1, y.y * f0 + o[r][1] * f1, y.z * f0 + o[r][2] * f1, y.w * f0 + o[r][3] * f1);
+      }
+      if (lane == 0) ml[r] = make_float2(M, x.y * f0 + l[r] * f1);
     }
+  }
+  __syncwarp();
 }
 
-// Rotates the lane's frequency pair of one token (x: channels f, f + 1; y: their partners f + d/2, ...) by
-// (c, s) and accumulates its products with the query fragments: three products of two-part operands, the
-// smallest (lo x lo) left out.
-__device__ inline void score_pair(float (&acc)[4], float2 x, float2 y, float2 c, float2 s, float2 ns, const uint32_t (&qh)[4],
-                                  const uint32_t (&ql)[4]) {
-  const float2 r = __ffma2_rn(x, c, __fmul2_rn(y, ns));
-  const float2 t = __ffma2_rn(y, c, __fmul2_rn(x, s));
-  uint32_t rh, rl, th, tl;
-  split_h2(r, rh, rl);
-  split_h2(t, th, tl);
-  mma_f16(acc, qh, rl, tl);
-  mma_f16(acc, ql, rh, th);
-  mma_f16(acc, qh, rh, th);
+// The lane's part of row `r`'s rotated query in fragment order: D / 4 lanes to a row, lane f2 a frequency
+// pair (x: its channels, y: their partners), scaled by a power of two to fp16's range.  *inv: its reciprocal.
+template <int D>
+__device__ __forceinline__ void query_pair(const Geo& g, const SharedArgs& a, const __nv_bfloat16* q, int p, int f2, float scale, bool live,
+                                           float2& x, float2& y, float* inv) {
+  constexpr int F = D / 2, LPR = D / 4;
+  const float4* rope4 = reinterpret_cast<const float4*>(a.rope);
+  x = y = make_float2(0.f, 0.f);
+  if (live) {
+    const uint32_t* qw = reinterpret_cast<const uint32_t*>(q);
+    const float2 q0 = b2_lohi(__ldg(qw + f2)), q1 = b2_lohi(__ldg(qw + f2 + F / 2));
+    const float4 u = __ldg(rope4 + (size_t)(p >> 3) * (F / 2) + f2), v = __ldg(rope4 + (size_t)(g.RC + (p & 7)) * (F / 2) + f2);
+    const float c0 = u.x * v.x - u.y * v.y, s0 = u.x * v.y + u.y * v.x;
+    const float c1 = u.z * v.z - u.w * v.w, s1 = u.z * v.w + u.w * v.z;
+    x = make_float2((q0.x * c0 - q1.x * s0) * scale, (q0.y * c1 - q1.y * s1) * scale);
+    y = make_float2((q1.x * c0 + q0.x * s0) * scale, (q1.y * c1 + q0.y * s1) * scale);
+  }
+  float mx = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const int e = fit_exp_f(mx);
+  const float qs = pow2i(e);
+  x = make_float2(x.x * qs, x.y * qs);
+  y = make_float2(y.x * qs, y.y * qs);
+  *inv = pow2i(-e);
 }
-
-__device__ inline float2 b2_lohi(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
 }  // namespace
 
 // One CTA per part and KV head, 8 warps.  The step slices of the head are staged once in shared memory, the
-// values as fp16 (scaled by a power of two, so that every bf16 value within 2^-28 of the largest is exact).
-// The tokens of a part are shared out over the warps in contiguous runs of 16-token tiles; a warp keeps its
-// own running softmax and outputs in registers, and the warps are joined at the end of an entry.
-//
-// Per tile, lane (j, quad) restores token j of each of the two pages: the entries of pair-groups
-// P = quad + 4 i straight into the B fragments of mma.sync m16n8k16 (the order of a dot product's channels is
-// free, so a fragment's k indices are the channels of the lane's own entries), rotated in fp32 by
-// e^{i p theta}, which moves on by one page (8 positions) with one complex multiplication.  Keys and queries
-// enter as sums of two fp16 values.  The value fragments need the channels in the lane's row instead: lane
-// (n, quad) takes channels [n d/8, (n + 1) d/8) of tokens 2 quad, 2 quad + 1 of both pages.
+// values as fp16 (scaled by a power of two, so that every bf16 value within 2^-28 of the largest is exact) in
+// rows padded by 16 bytes (8 tokens' entries of one group then fall on different banks as often as not).
 template <int D, int C>
 __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs a) {
   using X = Sh<D, C>;
@@ -306,30 +669,68 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   unsigned char* Ks = sm;
   unsigned char* Vs = sm + X::OFF_V;
   unsigned char* area = sm + X::OFF_W + warp * X::WARP;
-  uint4* Qf = reinterpret_cast<uint4*>(sm + X::OFF_Q);        // [hi, lo][k step][lane]
-  float4* Ff = reinterpret_cast<float4*>(sm + X::OFF_F);      // [frequency pair][lane]: (cos, cos, sin, sin) at S % 8 + j
-  float2* ml = reinterpret_cast<float2*>(sm + X::OFF_ML);     // [warp][row]
-  float* inv_s = reinterpret_cast<float*>(sm + X::OFF_INV);   // [row]
+  float* area_f = reinterpret_cast<float*>(area);
+  float4* Ff = reinterpret_cast<float4*>(sm + X::OFF_F);
+  float4* rrow = reinterpret_cast<float4*>(sm + X::OFF_R) + warp * (X::F / 2);
+  float2* ml_s = reinterpret_cast<float2*>(sm + X::OFF_ML);   // [warp][16]: rows of the area (own entries: 8, then 8 parked)
+  float2* ml = ml_s + warp * kQT;
+  float* inv_s = reinterpret_cast<float*>(sm + X::OFF_INV);
   uint32_t* red = reinterpret_cast<uint32_t*>(sm + X::OFF_RED);
-  long long* cut = reinterpret_cast<long long*>(sm + X::OFF_CUT);
   const uint32_t bar = smem_addr(sm + X::OFF_BAR);
   Counters c;
   c.ctx = reinterpret_cast<int*>(sm + X::OFF_C);
   c.coded = c.ctx + a.batch; c.own0 = c.coded + a.batch; c.gb = c.own0 + a.batch; c.sh = c.gb + a.ng + 1; c.lead = c.sh + a.ng;
+  const __nv_bfloat16* kslice = a.cbp + cbp_slice_off(g, a.layer, 0, blk, h, step_s);
+  const __nv_bfloat16* vslice = a.cbp + cbp_slice_off(g, a.layer, 1, blk, h, step_s);
 
+  // before the preceding kernel has ended only L2 is touched (and nothing is read through the read-only path that
+  // could move above the wait: counters and tables come by ld.global.cg)
   if (tid == 0) {
+    prefetch_l2(kslice, X::KS);
+    prefetch_l2(vslice, X::KS);
     mbar_init(bar, 1);
     fence_mbar_init();
+  }
+  dependency_wait();
+  dependents_may_launch();
+  if (tid == 0) {
     mbar_expect_tx(bar, 2 * X::KS);
-    bulk_g2s(smem_addr(Ks), a.cbp + cbp_slice_off(g, a.layer, 0, blk, h, step_s), X::KS, bar);
-    bulk_g2s(smem_addr(sm + X::OFF_W), a.cbp + cbp_slice_off(g, a.layer, 1, blk, h, step_s), X::KS, bar);
+    bulk_g2s(smem_addr(Ks), kslice, X::KS, bar);
+    bulk_g2s(smem_addr(sm + X::OFF_W), vslice, X::KS, bar);
   }
   const bool ok = load_counters(g, a, c, j == 0 && h == 0);   // (its barriers publish the mbarrier)
   // every slot of this part starts empty
   for (int i = tid; i < a.batch * rep * 2; i += kShThreads) {
     const int b = i / (rep * 2), r = i / 2 % rep;
-    a.pml[(((size_t)b * g.Hq + h * rep + r) * g.max_splits + j) * 2 + (i & 1)] = make_float2(-INFINITY, 0.f);
+    a.pml[(((size_t)b * g.Hq + h * rep + r) * g.max_splits + j) * 2 + (i & 1)] = make_float2(kNoMax, 0.f);
   }
+  Book<D, C> bk;
+  bk.Ks = Ks; bk.Vs = Vs; bk.Ff = Ff;
+  const float4* rope4 = reinterpret_cast<const float4*>(a.rope);   // two frequencies: (cos, sin, cos, sin)
+  auto pair_of = [&](int w) { return ((quad + 4 * (w / (C / 2))) * C + 2 * (w % (C / 2))) / 2; };   // lane's frequency pair w
+  if (warp < X::NW) {
+    const int p = (g.S & 7) + row;
+    const float4 x = __ldcg(rope4 + (size_t)(p >> 3) * (X::F / 2) + pair_of(warp));
+    const float4 y = __ldcg(rope4 + (size_t)(g.RC + (p & 7)) * (X::F / 2) + pair_of(warp));
+    Ff[warp * 32 + lane] = make_float4(x.x * y.x - x.y * y.y, x.z * y.z - x.w * y.w, x.x * y.y + x.y * y.x, x.z * y.w + x.w * y.z);
+  }
+#pragma unroll
+  for (int w = 0; w < X::NW; ++w) {
+    const float4 x = __ldcg(rope4 + X::F / 2 + pair_of(w));
+    bk.ec[w] = make_float2(x.x, x.z);
+    bk.es[w] = make_float2(x.y, x.w);
+  }
+  if (ok && g.pool) check_rows(g, a, c);
+  // this part of the head's list: [cut0, cut1), shared entries first
+  long long shared_total = 0, own_total = 0, before = 0, own_before = 0;
+  int e0 = 0;
+  if (ok) {
+    locate(g, c, a.ng, a.ng, a.ng + a.batch, 0, &own_before, &own_total);
+    locate(g, c, a.ng, 0, a.ng, 0, &before, &shared_total);
+  }
+  const long long cut0 = (shared_total + own_total) * j / a.k, cut1 = (shared_total + own_total) * (j + 1) / a.k;
+  if (ok) e0 = locate(g, c, a.ng, 0, a.ng, cut0, &before, &shared_total);
+
   const bool late = __syncthreads_or(!mbar_wait(bar, 0, g.wait_iters));
   if (late || !ok) {
     if (late && tid == 0) {
@@ -338,386 +739,147 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
     }
     return;
   }
-  if (g.pool) check_rows(g, a, c);
-  const int n_entries = a.ng + a.batch;
-  if (warp == 0) {
-    // the cut: costs summed lane by lane
-    const int per = (n_entries + 31) / 32;
-    long long mine = 0;
-    for (int e = lane * per; e < min(n_entries, (lane + 1) * per); ++e) mine += entry_of(g, c, a.ng, e).cost();
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) {
-      cut[0] = mine * j / a.k;
-      cut[1] = mine * (j + 1) / a.k;
+  // the slices' largest finite magnitudes (as bf16 pairs); the values go to their padded rows as scaled fp16
+  {
+    const uint4* kw = reinterpret_cast<const uint4*>(Ks);
+    const uint4* vw = reinterpret_cast<const uint4*>(sm + X::OFF_W);
+    auto amax = [](uint4 w, uint32_t m) {
+      m = __vmaxu2(m, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
+      return __vmaxu2(m, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+    };
+    auto finite = [](uint32_t w) {
+      w &= 0x7fff7fffu;
+      return ((w & 0xffffu) < 0x7f80u ? w & 0xffffu : 0u) | ((w >> 16) < 0x7f80u ? w & 0xffff0000u : 0u);
+    };
+    uint32_t ka = 0, va = 0;
+#pragma unroll 4
+    for (int i = tid; i < X::KS / 16; i += kShThreads) {
+      ka = amax(kw[i], ka);
+      va = amax(vw[i], va);
     }
-  }
-  // the slices' largest magnitudes; the values go to their padded rows as scaled fp16
-  uint32_t ka = 0, va = 0;
-  const uint32_t* kw = reinterpret_cast<const uint32_t*>(Ks);
-  const uint32_t* vw = reinterpret_cast<const uint32_t*>(sm + X::OFF_W);
-  for (int i = tid; i < X::KS / 4; i += kShThreads) {
-    ka = amax_b2(kw[i], ka);
-    va = amax_b2(vw[i], va);
-  }
-  ka = __reduce_max_sync(0xffffffffu, ka);
-  va = __reduce_max_sync(0xffffffffu, va);
-  if (lane == 0) { red[warp] = ka; red[kWarps + warp] = va; }
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) { ka = max(ka, red[w]); va = max(va, red[kWarps + w]); }
-  const int kexp = fit_exp(ka), vexp = fit_exp(va) + 1;
-  const float vscale = pow2i(vexp), vback = pow2i(-vexp);
-  for (int i = tid; i < X::KS / 4; i += kShThreads) {
-    const float2 v = b2_lohi(vw[i]);
-    *reinterpret_cast<uint32_t*>(Vs + (i / (D / 2)) * X::VROW + (i % (D / 2)) * 4) = pack_h2(v.x * vscale, v.y * vscale);
-  }
-  // e^{i (S % 8 + j) theta} per lane, and the lane's e^{i 8 theta}
-  const float4* rope4 = reinterpret_cast<const float4*>(a.rope);   // two frequencies: (cos, sin, cos, sin)
-  auto pair_of = [&](int w) { return ((quad + 4 * (w / (C / 2))) * C + 2 * (w % (C / 2))) / 2; };   // lane's frequency pair w
-  if (warp == 0) {
-#pragma unroll
-    for (int w = 0; w < X::NW; ++w) {
-      const int p = (g.S & 7) + row;
-      const float4 x = __ldg(rope4 + (size_t)(p >> 3) * (X::F / 2) + pair_of(w));
-      const float4 y = __ldg(rope4 + (size_t)(g.RC + (p & 7)) * (X::F / 2) + pair_of(w));
-      Ff[w * 32 + lane] = make_float4(x.x * y.x - x.y * y.y, x.z * y.z - x.w * y.w, x.x * y.y + x.y * y.x, x.z * y.w + x.w * y.z);
+    ka = max(ka & 0xffffu, ka >> 16);
+    va = max(va & 0xffffu, va >> 16);
+    if (__any_sync(0xffffffffu, max(ka, va) >= 0x7f80u)) {     // infinities or NaN among the entries: they count nothing
+      ka = va = 0;
+      for (int i = tid; i < X::KS / 4; i += kShThreads) {
+        const uint32_t k = finite(reinterpret_cast<const uint32_t*>(kw)[i]), v = finite(reinterpret_cast<const uint32_t*>(vw)[i]);
+        ka = max(ka, max(k & 0xffffu, k >> 16));
+        va = max(va, max(v & 0xffffu, v >> 16));
+      }
     }
-  }
-  float2 ec[X::NW], es[X::NW];
+    ka = __reduce_max_sync(0xffffffffu, ka);
+    va = __reduce_max_sync(0xffffffffu, va);
+    if (lane == 0) { red[warp] = ka; red[kWarps + warp] = va; }
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < X::NW; ++w) {
-    const float4 x = __ldg(rope4 + X::F / 2 + pair_of(w));
-    ec[w] = make_float2(x.x, x.z);
-    es[w] = make_float2(x.y, x.w);
+    for (int w = 0; w < kWarps; ++w) { ka = max(ka, red[w]); va = max(va, red[kWarps + w]); }
+    bk.ks = pow2i(fit_exp(ka));
+    bk.kinv = pow2i(-fit_exp(ka));
+    const float vscale = pow2i(fit_exp(va) + 1);
+#pragma unroll 4
+    for (int i = tid; i < X::KS / 16; i += kShThreads) {
+      const uint4 w = vw[i];
+      auto cv = [&](uint32_t x) { return pack_h2(bf16_lo(x) * vscale, bf16_hi(x) * vscale); };
+      *reinterpret_cast<uint4*>(Vs + (i / (D / 8)) * X::VROW + (i % (D / 8)) * 16) = make_uint4(cv(w.x), cv(w.y), cv(w.z), cv(w.w));
+    }
+    if (tid == 0) red[2 * kWarps] = __float_as_uint(pow2i(-fit_exp(va) - 1));
+    __syncthreads();
   }
-  __syncthreads();
-
+  const float vback = __uint_as_float(red[2 * kWarps]);
   const float qk_scale = 1.4426950408889634f / sqrtf((float)D);
-  long long at = 0;
-  for (int e = 0; e < n_entries; ++e) {
+  auto slot_of = [&](int b, int hq, int kind) { return (((size_t)b * g.Hq + hq) * g.max_splits + j) * 2 + kind; };
+
+  // ---- shared entries: the CTA's warps share out the tiles of one query tile at a time
+  long long at = before;
+  for (int e = e0; e < a.ng && at < cut1; ++e) {
     const Entry en = entry_of(g, c, a.ng, e);
     if (en.tiles == 0) continue;
-    const long long each = kOverhead + en.tiles;
-    const int q0 = cut[0] > at ? (int)min((long long)en.qtiles, (cut[0] - at) / each) : 0;
     const long long at0 = at;
     at += en.cost();
-    if (at <= cut[0]) continue;
-    if (at0 >= cut[1]) break;
-    const bool shared = e < a.ng;
-    const int lead = shared ? c.lead[e] : e - a.ng;
-    for (int qt = q0; qt < en.qtiles; ++qt) {
-      const long long base = at0 + qt * each + kOverhead;
-      const int t0 = (int)max(0ll, cut[0] - base), t1 = (int)min((long long)en.tiles, cut[1] - base);
-      if (base >= cut[1]) break;
+    for (int qt = cut0 > at0 ? (int)min((long long)en.qtiles, (cut0 - at0) / en.each()) : 0; qt < en.qtiles; ++qt) {
+      const long long base = at0 + qt * en.each() + en.fixed;
+      if (base >= cut1) break;
+      const int t0 = (int)max(0ll, cut0 - base), t1 = (int)min((long long)en.tiles, cut1 - base);
       if (t0 >= t1) continue;
       RowTile rt;
-      rt.b0 = shared ? c.gb[e] : lead;
+      rt.b0 = c.gb[e];
       rt.rep = rep; rt.r0 = qt * kQT; rt.h = h;
-      rt.nrows = min(kQT, (shared ? (c.gb[e + 1] - c.gb[e]) * rep : rep) - rt.r0);
-
-      // ---- query fragments: D / 4 lanes rotate a row at its own position, scale it to fp16's range and split it
+      rt.nrows = min(kQT, (c.gb[e + 1] - c.gb[e]) * rep - rt.r0);
       {
-        constexpr int LPR = D / 4, RPW = 32 / LPR;            // lanes of a row, rows a warp takes at once
-        const int f2 = lane % LPR;                            // frequency pair
-        const int P = 2 * f2 / C, sub = 2 * f2 % C / 2;       // its pair-group and place: fragment lane and k step
+        uint4* Qf = reinterpret_cast<uint4*>(sm + X::OFF_W);   // [hi, lo][k step][lane], in the first warps' areas
+        constexpr int LPR = D / 4, RPW = 32 / LPR;             // lanes of a row, rows a warp takes at once
+        const int f2 = lane % LPR, P = 2 * f2 / C, sub = 2 * f2 % C / 2;
         for (int r = warp * RPW + lane / LPR; r < kQT; r += kWarps * RPW) {
-          float2 x = make_float2(0.f, 0.f), y = x;
-          if (r < rt.nrows && c.ctx[rt.request(r)] > 0) {
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + ((size_t)rt.request(r) * g.Hq + rt.head(r)) * D);
-            const int p = c.ctx[rt.request(r)] - 1;
-            const float2 q0v = b2_lohi(__ldg(q + f2)), q1v = b2_lohi(__ldg(q + f2 + X::F / 2));
-            const float4 u = __ldg(rope4 + (size_t)(p >> 3) * (X::F / 2) + f2);
-            const float4 v = __ldg(rope4 + (size_t)(g.RC + (p & 7)) * (X::F / 2) + f2);
-            const float c0 = u.x * v.x - u.y * v.y, s0 = u.x * v.y + u.y * v.x;
-            const float c1 = u.z * v.z - u.w * v.w, s1 = u.z * v.w + u.w * v.z;
-            x = make_float2((q0v.x * c0 - q1v.x * s0) * qk_scale, (q0v.y * c1 - q1v.y * s1) * qk_scale);
-            y = make_float2((q1v.x * c0 + q0v.x * s0) * qk_scale, (q1v.y * c1 + q0v.y * s1) * qk_scale);
-          }
-          float mx = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int qe = mx > 0.f && mx < INFINITY ? min(13 - (((__float_as_int(mx) >> 23) & 255) - 127), 90) : 0;
-          const float qs = pow2i(qe);
+          const bool live = r < rt.nrows && c.ctx[rt.request(r)] > 0;
+          float2 x, y;
+          float inv;
+          query_pair<D>(g, a, live ? a.q + ((size_t)rt.request(r) * g.Hq + rt.head(r)) * D : a.q, live ? c.ctx[rt.request(r)] - 1 : 0, f2,
+                        qk_scale, live, x, y, &inv);
           uint32_t xh, xl, yh, yl;
-          split_h2(make_float2(x.x * qs, x.y * qs), xh, xl);
-          split_h2(make_float2(y.x * qs, y.y * qs), yh, yl);
+          split_h2(x, xh, xl);
+          split_h2(y, yh, yl);
           const int ks = P / 4 * (C / 2) + sub, fl = (r & 7) * 4 + P % 4, rg = r >> 3;
           uint32_t* fh = reinterpret_cast<uint32_t*>(Qf + ks * 32 + fl);
           uint32_t* fw = reinterpret_cast<uint32_t*>(Qf + (X::NW + ks) * 32 + fl);
           fh[rg] = xh; fh[rg + 2] = yh;
           fw[rg] = xl; fw[rg + 2] = yl;
-          if (f2 == 0) inv_s[r] = pow2i(-qe);
+          if (f2 == 0) inv_s[r] = inv;
         }
       }
       __syncthreads();
-      uint32_t qh[X::NW][4], ql[X::NW][4];
+      uint32_t qf[2][X::NW][4];
 #pragma unroll
-      for (int w = 0; w < X::NW; ++w) {
-        const uint4 u = Qf[w * 32 + lane], v = Qf[(X::NW + w) * 32 + lane];
-        qh[w][0] = u.x; qh[w][1] = u.y; qh[w][2] = u.z; qh[w][3] = u.w;
-        ql[w][0] = v.x; ql[w][1] = v.y; ql[w][2] = v.z; ql[w][3] = v.w;
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int w = 0; w < X::NW; ++w) {
+          const uint4 u = reinterpret_cast<const uint4*>(sm + X::OFF_W)[(i * X::NW + w) * 32 + lane];
+          qf[i][w][0] = u.x; qf[i][w][1] = u.y; qf[i][w][2] = u.z; qf[i][w][3] = u.w;
+        }
       const float qinv[2] = {inv_s[row], inv_s[row + 8]};
+      __syncthreads();                                         // the fragments are read
       State<D, C> st;
-#pragma unroll
-      for (int i = 0; i < X::NT; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) st.o[i][k] = 0.f;
-      st.m[0] = st.m[1] = -1e30f;
-      st.l[0] = st.l[1] = 0.f;
-
-      // ---- this warp's tiles, by source
+      st.clear();
       const int w0 = t0 + (int)((long long)(t1 - t0) * warp / kWarps), w1 = t0 + (int)((long long)(t1 - t0) * (warp + 1) / kWarps);
-      // source ranges of the entry's tile list: [0, ns) sink, [ns, nc) coded, [nc, tiles) recent
-      const int ctx = shared ? 0 : c.ctx[lead];
-      const int S_eff = min(g.S, ctx), n_sink_t = ceil_div(S_eff, kTT);
-      const int cod0 = shared ? 0 : c.own0[lead], n_cod = shared ? c.sh[e] : c.coded[lead] - cod0;
-      const int n_cod_t = n_sink_t + ceil_div(n_cod, kTT);
-
-      // coded tiles
-      const int ca = max(w0, n_sink_t), cb = min(w1, n_cod_t);
-      if (ca < cb) {
-        const uint8_t* kcode = a.idx + idx_page_off(g, a.layer, blk, lead, h, 0, 0);
-        const uint8_t* vcode = a.idx + idx_page_off(g, a.layer, blk, lead, h, 1, 0);
-        const int pg0 = cod0 / kPage + 2 * (ca - n_sink_t), pg_end = (cod0 + n_cod + kPage - 1) / kPage;
-        const float inv[2] = {qinv[0] * pow2i(-kexp), qinv[1] * pow2i(-kexp)};
-        int ids = 0, ids_at = -32;                             // physical pages [ids_at, ids_at + 32) of the run, one a lane
-        auto fetch = [&](int t) {                              // the codes of run tile t into its stage
-          const int pp = 2 * t;
-          if (pp - ids_at >= 32) {
-            ids_at = pp;
-            ids = phys_page(g, lead, min(pg0 + pp + lane, pg_end - 1));
-            if (ids < 0) {
-              set_status(a.st, LVQ_ECAPACITY);
-              ids = 0;
-            }
-          }
-          const int i0 = __shfl_sync(0xffffffffu, ids, pp - ids_at), i1 = __shfl_sync(0xffffffffu, ids, pp + 1 - ids_at);
-          const uint32_t dst = smem_addr(area) + (t % X::NST) * X::STAGE;
-          constexpr int VP = X::PAGE / 16;
-#pragma unroll
-          for (int v = lane; v < 4 * VP; v += 32) {
-            const int id = (v / VP) & 1 ? i1 : i0;
-            cp_async16(dst + v * 16, (v < 2 * VP ? kcode : vcode) + (size_t)id * X::PAGE + v % VP * 16);
-          }
-        };
-        const int nt = cb - ca;
-#pragma unroll
-        for (int t = 0; t < X::NST - 1; ++t) {
-          if (t < nt) fetch(t);
-          cp_commit();
-        }
-        float2 wc[X::NW], ws[X::NW];
-        for (int t = 0; t < nt; ++t) {
-          cp_wait<X::NST - 2>();
-          __syncwarp();
-          if (t % 8 == 0) {
-            // e^{i p theta} anew from the tables every 16 pages: the recurrence's rounding does not grow further
-            const int p8 = pg0 + 2 * t + (g.S >> 3);
-            const float ks = pow2i(kexp);
-#pragma unroll
-            for (int w = 0; w < X::NW; ++w) {
-              const float4 x = __ldg(rope4 + (size_t)p8 * (X::F / 2) + pair_of(w));
-              const float4 y = Ff[w * 32 + lane];
-              wc[w] = make_float2((x.x * y.x - x.y * y.z) * ks, (x.z * y.y - x.w * y.w) * ks);
-              ws[w] = make_float2((x.x * y.z + x.y * y.x) * ks, (x.z * y.w + x.w * y.y) * ks);
-            }
-          }
-          const unsigned char* codes = area + (t % X::NST) * X::STAGE;
-          float s[2][4] = {};
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-#pragma unroll
-            for (int i = 0; i < X::NI; ++i) {
-              const int P = quad + 4 * i;
-              const uint32_t k0 = codes[u * X::PAGE + P * kPage + row], k1 = codes[u * X::PAGE + (P + X::NP) * kPage + row];
-              const unsigned char* e0 = Ks + k0 * (2 * D) + P * (2 * C);
-              const unsigned char* e1 = Ks + k1 * (2 * D) + (P + X::NP) * (2 * C);
-#pragma unroll
-              for (int q = 0; q < (C + 7) / 8; ++q) {
-                uint32_t lo[4], hi[4];
-                if constexpr (C == 4) {
-                  const uint2 x = *reinterpret_cast<const uint2*>(e0), y = *reinterpret_cast<const uint2*>(e1);
-                  lo[0] = x.x; lo[1] = x.y; hi[0] = y.x; hi[1] = y.y;
-                } else {
-                  const uint4 x = *reinterpret_cast<const uint4*>(e0 + 16 * q), y = *reinterpret_cast<const uint4*>(e1 + 16 * q);
-                  lo[0] = x.x; lo[1] = x.y; lo[2] = x.z; lo[3] = x.w;
-                  hi[0] = y.x; hi[1] = y.y; hi[2] = y.z; hi[3] = y.w;
-                }
-#pragma unroll
-                for (int v = 0; v < (C < 8 ? C / 2 : 4); ++v) {
-                  const int w = i * (C / 2) + q * 4 + v;
-                  const float2 ns = neg2(ws[w]);
-                  score_pair(s[u], b2_lohi(lo[v]), b2_lohi(hi[v]), wc[w], ws[w], ns, qh[w], ql[w]);
-                  const float2 cn = __ffma2_rn(wc[w], ec[w], __fmul2_rn(ns, es[w]));
-                  ws[w] = __ffma2_rn(ws[w], ec[w], __fmul2_rn(wc[w], es[w]));
-                  wc[w] = cn;
-                }
-              }
-            }
-          }
-          const int n = min(kTT, n_cod - (ca - n_sink_t + t) * kTT);
-          softmax_tile<D, C>(st, s, inv, n, quad);
-          uint32_t ph[4], pl[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) split_h2(make_float2(s[k >> 1][2 * (k & 1)], s[k >> 1][2 * (k & 1) + 1]), ph[k], pl[k]);
-          // values: channels row * d/8 + 8 q ... of tokens 2 quad, 2 quad + 1 of both pages
-          const unsigned char* vc = codes + 2 * X::PAGE + 2 * quad;
-          const bool ragged = n < kTT;
-#pragma unroll
-          for (int q = 0; q < D / 64; ++q) {
-            uint32_t v[4][4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-              for (int part = 0; part < (C == 4 ? 2 : 1); ++part) {
-                const int grp = (row * (D / 8) + 8 * q + 4 * part) / C;
-                uint32_t two = *reinterpret_cast<const uint16_t*>(vc + u * X::PAGE + grp * kPage);
-                uint32_t c0 = two & 255u, c1 = two >> 8;
-                if (ragged) {                                 // masked tokens take the first token's entry: nothing else is read
-                  const uint32_t first = codes[2 * X::PAGE + grp * kPage];
-                  if (8 * u + 2 * quad >= n) c0 = first;
-                  if (8 * u + 2 * quad + 1 >= n) c1 = first;
-                }
-                const int off = C == 4 ? grp * 8 : (row * (D / 8) + 8 * q) * 2;
-                const unsigned char *r0 = Vs + c0 * X::VROW + off, *r1 = Vs + c1 * X::VROW + off;
-                if constexpr (C == 4) {
-                  const uint2 x = *reinterpret_cast<const uint2*>(r0), y = *reinterpret_cast<const uint2*>(r1);
-                  v[2 * u][2 * part] = x.x; v[2 * u][2 * part + 1] = x.y;
-                  v[2 * u + 1][2 * part] = y.x; v[2 * u + 1][2 * part + 1] = y.y;
-                } else {
-                  const uint4 x = *reinterpret_cast<const uint4*>(r0), y = *reinterpret_cast<const uint4*>(r1);
-                  v[2 * u][0] = x.x; v[2 * u][1] = x.y; v[2 * u][2] = x.z; v[2 * u][3] = x.w;
-                  v[2 * u + 1][0] = y.x; v[2 * u + 1][1] = y.y; v[2 * u + 1][2] = y.z; v[2 * u + 1][3] = y.w;
-                }
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t sel = i & 1 ? 0x7632u : 0x5410u;
-              const uint32_t b0 = __byte_perm(v[0][i >> 1], v[1][i >> 1], sel), b1 = __byte_perm(v[2][i >> 1], v[3][i >> 1], sel);
-              mma_f16(st.o[8 * q + i], pl, b0, b1);
-              mma_f16(st.o[8 * q + i], ph, b0, b1);
-            }
-          }
-          __syncwarp();                                       // the stage is read
-          if (t + X::NST - 1 < nt) fetch(t + X::NST - 1);
-          cp_commit();
-        }
-        cp_wait<0>();
-        __syncwarp();
+      if (w0 < w1) {
+        Run run;
+        run.lead = c.lead[e];
+        run.pg0 = 2 * w0;
+        run.n = min(w1 * kTT, c.sh[e]) - w0 * kTT;
+        run.pg_end = run.pg0 + ceil_div(run.n, kPage);
+        run.kcode = a.idx + idx_page_off(g, a.layer, blk, run.lead, h, 0, 0);
+        run.vcode = a.idx + idx_page_off(g, a.layer, blk, run.lead, h, 1, 0);
+        coded_run<D, C, false>(g, a, bk, run, st, qf, qinv, area, rrow);
       }
-
-      // bf16 tiles: the sink's, then the recent window's
-#pragma unroll 1
-      for (int src = 0; src < 2; ++src) {
-        const int ra = src == 0 ? w0 : max(w0, n_cod_t), rb = src == 0 ? min(w1, n_sink_t) : w1;
-        if (shared) break;
-        const int total = src == 0 ? S_eff : ctx - S_eff - c.coded[lead];
-#pragma unroll 1
-        for (int t = ra; t < rb; ++t) {
-          const int i0 = (t - (src == 0 ? 0 : n_cod_t)) * kTT, n = min(kTT, total - i0);
-          // rows [K, V][16][d] of the tile; rows that hold no token are zero
-          for (int v = lane; v < 2 * kTT * (D / 8); v += 32) {
-            const int kv = v / (kTT * (D / 8)), tok = v / (D / 8) % kTT, col = v % (D / 8);
-            if (tok < n) {
-              const __nv_bfloat16* src_row = src == 0 ? a.sink + sink_off(g, a.layer, kv, a.step, lead, h, i0 + tok)
-                                                      : a.ring + ring_off(g, a.layer, kv, a.step, lead, h, (c.coded[lead] + i0 + tok) % g.R);
-              cp_async16(smem_addr(area) + v * 16, src_row + col * 8);
-            } else {
-              *reinterpret_cast<uint4*>(area + v * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
-          cp_commit();
-          cp_wait<0>();
-          __syncwarp();
-          const int p0 = (src == 0 ? 0 : g.S + c.coded[lead]) + i0 + row;
-          float s[2][4] = {};
-          uint32_t am = 0;
-          for (int v = lane; v < kTT * D / 2; v += 32) am = amax_b2(reinterpret_cast<const uint32_t*>(area)[v], am);
-          const int te = fit_exp(__reduce_max_sync(0xffffffffu, am));
-          const float ts = pow2i(te);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            // (a row past the last token is zero: its position only has to lie within the tables)
-            const int p = min(p0 + 8 * u, g.max_ctx - 1);
-#pragma unroll
-            for (int w = 0; w < X::NW; ++w) {
-              const float4 x = __ldg(rope4 + (size_t)(p >> 3) * (X::F / 2) + pair_of(w));
-              const float4 y = __ldg(rope4 + (size_t)(g.RC + (p & 7)) * (X::F / 2) + pair_of(w));
-              const float2 cc = make_float2((x.x * y.x - x.y * y.y) * ts, (x.z * y.z - x.w * y.w) * ts);
-              const float2 sc = make_float2((x.x * y.y + x.y * y.x) * ts, (x.z * y.w + x.w * y.z) * ts);
-              const uint32_t* kr = reinterpret_cast<const uint32_t*>(area) + (8 * u + row) * (D / 2);
-              score_pair(s[u], b2_lohi(kr[pair_of(w)]), b2_lohi(kr[pair_of(w) + X::F / 2]), cc, sc, neg2(sc), qh[w], ql[w]);
-            }
-          }
-          const float inv[2] = {qinv[0] * pow2i(-te), qinv[1] * pow2i(-te)};
-          softmax_tile<D, C>(st, s, inv, n, quad);
-          // bf16 values are exact as they are; the weights as three bf16 parts, in the outputs' scale
-          uint32_t pp[3][4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float x = s[k >> 1][2 * (k & 1)] * vscale, y = s[k >> 1][2 * (k & 1) + 1] * vscale;
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-              pp[i][k] = pack_b2(x, y);
-              x -= bf16_lo(pp[i][k]);
-              y -= bf16_hi(pp[i][k]);
-            }
-          }
-          const uint32_t* vr = reinterpret_cast<const uint32_t*>(area) + kTT * (D / 2) + row * (D / 16);
-#pragma unroll
-          for (int q = 0; q < X::NT / 2; ++q) {
-            const uint32_t x0 = vr[2 * quad * (D / 2) + q], x1 = vr[(2 * quad + 1) * (D / 2) + q];
-            const uint32_t y0 = vr[(2 * quad + 8) * (D / 2) + q], y1 = vr[(2 * quad + 9) * (D / 2) + q];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t sel = i ? 0x7632u : 0x5410u;
-              const uint32_t b0 = __byte_perm(x0, x1, sel), b1 = __byte_perm(y0, y1, sel);
-#pragma unroll
-              for (int k = 2; k >= 0; --k) mma_bf16(st.o[2 * q + i], pp[k], b0, b1);
-            }
-          }
-          __syncwarp();
-        }
-      }
-
-      // ---- the warps' results are joined
+      // the warps' results are joined
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 1);
         st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 2);
-        if (quad == 0) ml[warp * kQT + row + 8 * r] = make_float2(st.m[r], st.l[r]);
+        if (quad == 0) ml[row + 8 * r] = make_float2(st.m[r], st.l[r]);
+        float* to = area_f + (row + 8 * r) * X::OROW;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          float* to = reinterpret_cast<float*>(area) + (row + 8 * r) * X::OROW + (2 * quad + n) * X::NT;
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int i = 0; i < X::NT; i += 4)
-            *reinterpret_cast<float4*>(to + i) =
-                make_float4(st.o[i][2 * r + n], st.o[i + 1][2 * r + n], st.o[i + 2][2 * r + n], st.o[i + 3][2 * r + n]);
-        }
+          for (int i = 0; i < X::NT; ++i) to[out_channel<D, C>(i, 2 * quad + n)] = st.o[i][2 * r + n];
       }
       __syncthreads();
       {
-        constexpr int TPR = kShThreads / kQT, CH = D / TPR;   // threads of a row, channels of a thread
+        constexpr int TPR = kShThreads / kQT, CH = D / TPR;    // threads of a row, channels of a thread
         const int r = tid / TPR, c0 = tid % TPR * CH;
         if (r < rt.nrows && c.ctx[rt.request(r)] > 0) {
-          float M = -1e30f, L = 0.f, o[CH] = {};
+          float M = kNoMax, L = 0.f, o[CH] = {};
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w)
-            if (ml[w * kQT + r].y > 0.f) M = fmaxf(M, ml[w * kQT + r].x);
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml_s[w * kQT + r].x);
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float2 x = ml[w * kQT + r];
-            const float f = x.y > 0.f ? ex2(x.x - M) : x.y;   // (a NaN sum stays one)
+            const float2 x = ml_s[w * kQT + r];
+            const float f = ex2(x.x - M);
             L += f * x.y;
             const float* from = reinterpret_cast<const float*>(sm + X::OFF_W + w * X::WARP) + r * X::OROW + c0;
-            if (x.y > 0.f || x.y != x.y)
 #pragma unroll
-              for (int i = 0; i < CH; ++i) o[i] += (x.y > 0.f ? f : x.y) * from[i];
+            for (int i = 0; i < CH; ++i) o[i] += f * from[i];
           }
-          const size_t slot = (((size_t)rt.request(r) * g.Hq + rt.head(r)) * g.max_splits + j) * 2 + !shared;
+          const size_t slot = slot_of(rt.request(r), rt.head(r), 0);
 #pragma unroll
           for (int i = 0; i < CH; i += 4)
             *reinterpret_cast<float4*>(a.po + slot * D + c0 + i) =
@@ -728,34 +890,204 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
       __syncthreads();
     }
   }
+
+  // ---- own entries: a contiguous run of the part's tiles to a warp
+  const long long o0 = max(0ll, cut0 - shared_total), o1 = max(0ll, cut1 - shared_total);
+  if (o0 >= o1) return;
+  const long long x0 = o0 + (o1 - o0) * warp / kWarps, x1 = o0 + (o1 - o0) * (warp + 1) / kWarps;
+  int* park_s = reinterpret_cast<int*>(red) + 2 * kWarps;      // [warp]: entry tile whose beginning another warp has, or -1
+  int* last_s = reinterpret_cast<int*>(red) + kWarps;          // [warp]: its last tile of that entry ends the part's share
+  int park = -1, open = -1, open_b = 0, open_qt = 0, ended = 0, any = 0;   // open: the last piece, which other warps continue
+  __syncthreads();                                             // (red is reused)
+  if (x0 < x1) {
+    int e = locate(g, c, a.ng, a.ng, a.ng + a.batch, x0, &own_before, &own_total);
+    long long eat = own_before;
+    for (; e < a.ng + a.batch && eat < x1; ++e) {
+      const Entry en = entry_of(g, c, a.ng, e);
+      if (en.tiles == 0) continue;
+      const int b = e - a.ng;
+      for (int qt = x0 > eat ? (int)min((long long)en.qtiles, (x0 - eat) / en.each()) : 0; qt < en.qtiles; ++qt) {
+        const long long base = eat + qt * en.each() + en.fixed;
+        if (base >= x1) break;
+        const int ta = (int)max(0ll, x0 - base), tb = (int)min((long long)en.tiles, x1 - base);
+        if (ta >= tb) continue;
+        const int Ta = (int)max(0ll, o0 - base), Tb = (int)min((long long)en.tiles, o1 - base);   // the part's share
+        any = 1;
+        const int nrows = min(kOT, rep - qt * kOT);
+        const __nv_bfloat16* q = a.q + ((size_t)b * g.Hq + h * rep + qt * kOT) * D;
+        const int own0 = c.own0[b], rest = c.coded[b] - own0, nc = ceil_div(rest, kTT);
+        const bool coded = ta < nc;
+        if (coded) {
+          uint4* Qf = reinterpret_cast<uint4*>(area);          // [k step][lane]: high parts in registers 0, 2, low in 1, 3
+          constexpr int LPR = D / 4, RPW = 32 / LPR;
+          const int f2 = lane % LPR, P = 2 * f2 / C, sub = 2 * f2 % C / 2;
+          for (int r0 = 0; r0 < nrows; r0 += RPW) {
+            const int r = r0 + lane / LPR;
+            float2 x, y;
+            float inv;
+            query_pair<D>(g, a, q + (size_t)min(r, nrows - 1) * D, c.ctx[b] - 1, f2, qk_scale, true, x, y, &inv);
+            uint4 f;
+            split_h2(x, f.x, f.y);
+            split_h2(y, f.z, f.w);
+            if (r < nrows) {
+              Qf[(P / 4 * (C / 2) + sub) * 32 + r * 4 + P % 4] = f;
+              if (f2 == 0) ml[r].x = inv;
+            }
+          }
+          __syncwarp();
+          uint32_t qf[1][X::NW][4];
+#pragma unroll
+          for (int w = 0; w < X::NW; ++w) {
+            const uint4 u = row < nrows ? Qf[w * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
+            qf[0][w][0] = u.x; qf[0][w][1] = u.y; qf[0][w][2] = u.z; qf[0][w][3] = u.w;
+          }
+          const float qi = row < nrows ? ml[row].x : 1.f;
+          const float qinv[2] = {qi, qi};
+          __syncwarp();
+          State<D, C> st;
+          st.clear();
+          Run run;
+          run.lead = b;
+          run.pg0 = own0 / kPage + 2 * ta;
+          run.n = min(min(tb, nc) * kTT, rest) - ta * kTT;
+          run.pg_end = run.pg0 + ceil_div(run.n, kPage);
+          run.kcode = a.idx + idx_page_off(g, a.layer, blk, b, h, 0, 0);
+          run.vcode = a.idx + idx_page_off(g, a.layer, blk, b, h, 1, 0);
+          coded_run<D, C, true>(g, a, bk, run, st, qf, qinv, area, rrow);
+          st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], 1);
+          st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], 2);
+          if (row < nrows) {
+            if (quad == 0) ml[row] = make_float2(st.m[0], st.l[0]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int i = 0; i < X::NT; ++i)
+                area_f[row * X::OROW + out_channel<D, C>(i, 2 * quad + n)] = (st.o[i][n] + st.o[i][2 + n]) * vback;
+          }
+          __syncwarp();
+        }
+        if (tb > nc) {
+          const int i0 = max(ta - nc, 0) * kTT, i1 = min((tb - nc) * kTT, c.ctx[b] - c.coded[b]);
+          int r = 0;
+          for (; r + 4 <= nrows; r += 4)
+            bf16_run<D, C, 4>(g, a, c, b, h, q + (size_t)r * D, qk_scale, i0, i1, area_f + r * X::OROW, ml + r, !coded);
+          for (; r < nrows; ++r)
+            bf16_run<D, C, 1>(g, a, c, b, h, q + (size_t)r * D, qk_scale, i0, i1, area_f + r * X::OROW, ml + r, !coded);
+        }
+        const int id = b * en.qtiles + qt;
+        if (ta > Ta) {
+          // another warp has the beginning: parked for it
+          for (int r = 0; r < nrows; ++r)
+            for (int i = lane; i < D; i += 32) area_f[X::PARK / 4 + r * X::OROW + i] = area_f[r * X::OROW + i];
+          if (lane < nrows) ml[kOT + lane] = ml[lane];
+          park = id;
+          ended = tb == Tb;
+        } else if (tb < Tb) {
+          open = id;
+          open_b = b; open_qt = qt;
+        } else {
+          for (int r = 0; r < nrows; ++r) {
+            const size_t slot = slot_of(b, h * rep + qt * kOT + r, 1);
+            for (int i = lane; i < D / 4; i += 32)
+              *reinterpret_cast<float4*>(a.po + slot * D + 4 * i) = *reinterpret_cast<const float4*>(area_f + r * X::OROW + 4 * i);
+            if (lane == 0) a.pml[slot] = ml[r];
+          }
+        }
+        __syncwarp();
+      }
+      eat += en.cost();
+    }
+  }
+  if (lane == 0) {
+    park_s[warp] = any ? park : -2;                            // -2: no tile at all
+    last_s[warp] = ended;
+  }
+  __syncthreads();
+  if (open >= 0) {
+    const int nrows = min(kOT, rep - open_qt * kOT);
+    for (int r = 0; r < nrows; ++r) {
+      float M = ml[r].x, L = 0.f;
+      int wl = warp;                                           // warps (warp, wl] continue the entry
+      for (int w = warp + 1; w < kWarps; ++w) {
+        if (park_s[w] == -2) continue;
+        if (park_s[w] != open) break;
+        wl = w;
+        M = fmaxf(M, ml_s[w * kQT + kOT + r].x);
+        if (last_s[w]) break;
+      }
+      const size_t slot = slot_of(open_b, h * rep + open_qt * kOT + r, 1);
+      float o[D / 32];
+      const float f0 = ex2(ml[r].x - M);
+      L = ml[r].y * f0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] = area_f[r * X::OROW + lane + 32 * i] * f0;
+      for (int w = warp + 1; w <= wl; ++w) {
+        if (park_s[w] != open) continue;
+        const float2 x = ml_s[w * kQT + kOT + r];
+        const float f = ex2(x.x - M);
+        L += f * x.y;
+        const float* from = reinterpret_cast<const float*>(sm + X::OFF_W + w * X::WARP + X::PARK) + r * X::OROW;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] += f * from[lane + 32 * i];
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) a.po[slot * D + lane + 32 * i] = o[i];
+      if (lane == 0) a.pml[slot] = make_float2(M, L);
+    }
+  }
 }
 
-// Joins the partials of one (request, query head): thread e owns output element e.
+// Joins the partials of a (request, query head): a warp each, a lane d / 32 channels.
 template <int D>
-__global__ void __launch_bounds__(D) shared_merge_kernel(Geo g, int k, const float* __restrict__ po,
-                                                         const float2* __restrict__ pml, float* __restrict__ out,
-                                                         float* __restrict__ lse) {
-  const int hq = blockIdx.x, b = blockIdx.y, e = threadIdx.x;
-  const size_t row = (size_t)b * g.Hq + hq, slot0 = row * g.max_splits * 2;
-  float M = -INFINITY;
-  for (int i = 0; i < 2 * k; ++i)
-    if (pml[slot0 + i].y != 0.f) M = fmaxf(M, pml[slot0 + i].x);
-  float den = 0.f, acc = 0.f;
-  if (M != -INFINITY)
-    for (int i = 0; i < 2 * k; ++i) {
-      const float2 ml = pml[slot0 + i];
-      if (ml.y != 0.f) {
-        const float w = exp2f(ml.x - M);
-        den = fmaf(w, ml.y, den);
-        acc = fmaf(w, po[(slot0 + i) * D + e], acc);
+__global__ void __launch_bounds__(128) shared_merge_kernel(Geo g, int rows, int k, const float* po, const float2* pml, float* out,
+                                                           float* lse) {
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  dependency_wait();
+  dependents_may_launch();
+  if (r >= rows) return;
+  const size_t slot0 = (size_t)r * g.max_splits * 2;
+  float M = kNoMax;
+  for (int i = lane; i < 2 * k; i += 32) {
+    const float2 x = __ldcg(pml + slot0 + i);
+    if (x.y != 0.f) M = fmaxf(M, x.x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float den = 0.f, acc[V] = {};
+  for (int i0 = 0; i0 < 2 * k; i0 += 32) {
+    const float2 x = i0 + lane < 2 * k ? __ldcg(pml + slot0 + i0 + lane) : make_float2(kNoMax, 0.f);
+    const float w = x.y != 0.f ? ex2(x.x - M) : 0.f;
+    den += w * x.y;
+    unsigned todo = __ballot_sync(0xffffffffu, x.y != 0.f);
+    while (todo) {                                             // four partials at a time, in slot order
+      float f[4];
+      float v[4][V];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = todo ? __ffs(todo) - 1 : -1;
+        todo &= todo - 1;
+        f[u] = __shfl_sync(0xffffffffu, w, i < 0 ? 0 : i);
+        if (i < 0) f[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[u][e] = i < 0 ? 0.f : __ldcg(po + (slot0 + i0 + i) * D + lane * V + e);
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(f[u], v[u][e], acc[e]);
     }
-  out[row * D + e] = den != 0.f ? acc / den : 0.f;
-  if (e == 0) lse[row] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+#pragma unroll
+  for (int e = 0; e < V; ++e) out[(size_t)r * D + lane * V + e] = den != 0.f ? acc[e] / den : 0.f;
+  if (lane == 0) lse[r] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <int D, int C>
-static cudaError_t shared_as(const Geo& g, const SharedArgs& a, float* out, float* lse, cudaStream_t s) {
+static cudaError_t shared_as(const Geo& g, SharedArgs a, float* out, float* lse, cudaStream_t s) {
   static bool attr_set[kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -766,11 +1098,24 @@ static cudaError_t shared_as(const Geo& g, const SharedArgs& a, float* out, floa
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) attr_set[dev] = true;
   }
-  shared_kernel<D, C><<<dim3(a.k, g.H), kShThreads, Sh<D, C>::smem(a.batch, a.ng), s>>>(g, a);
-  e = cudaGetLastError();
+  // both kernels may start while the one before them ends, and wait for it before they read or write anything
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(a.k, g.H);
+  lc.blockDim = dim3(kShThreads);
+  lc.dynamicSmemBytes = Sh<D, C>::smem(a.batch, a.ng);
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  e = cudaLaunchKernelEx(&lc, shared_kernel<D, C>, g, a);
   if (e != cudaSuccess) return e;
-  shared_merge_kernel<D><<<dim3(g.Hq, a.batch), D, 0, s>>>(g, a.k, a.po, a.pml, out, lse);
-  return cudaGetLastError();
+  const int rows = a.batch * g.Hq;
+  lc.gridDim = dim3((rows + 3) / 4);
+  lc.blockDim = dim3(128);
+  lc.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&lc, shared_merge_kernel<D>, g, rows, a.k, (const float*)a.po, (const float2*)a.pml, out, lse);
 }
 
 cudaError_t launch_decode_shared(const Geo& g, int layer, int step, int batch, const __nv_bfloat16* q,
