@@ -365,7 +365,7 @@ LVQ_API lvq_status lvq_copy_pages(const lvq_config* cfg, const lvq_layout* lay, 
  *   page_table: cfg->page_table, writable.  Every entry that names a page becomes that page's
  *     new id; the others stay.
  * Pages that no move writes keep their contents. */
-#define LVQ_MOVE_SLAB 128
+#define LVQ_MOVE_SLAB 64
 #define LVQ_PAGE_HOLD (-1)
 LVQ_API lvq_status lvq_compact_pages(const lvq_config* cfg, const lvq_layout* lay, int32_t n_moves,
                                      const int32_t* moves, const int32_t* new_id,

@@ -81,10 +81,10 @@ cudaError_t launch_copy_pages(const Geo& g, int n, const int32_t* pairs, uint8_t
 // issued before this slab's writes, and the list streams at full memory parallelism.
 // CTAs past the last stream rewrite the page table.
 template <int CW>
-__global__ void __launch_bounds__(kThreads) compact_pages_kernel(Geo g, int n_moves, int n_move_ctas,
-                                                                 const int2* __restrict__ moves,
-                                                                 const int32_t* __restrict__ new_id,
-                                                                 int32_t* table, uint8_t* idx, int32_t* st) {
+__global__ void __launch_bounds__(kThreads, 6) compact_pages_kernel(Geo g, int n_moves, int n_move_ctas,
+                                                                    const int2* __restrict__ moves,
+                                                                    const int32_t* __restrict__ new_id,
+                                                                    int32_t* table, uint8_t* idx, int32_t* st) {
   constexpr int U = LVQ_MOVE_SLAB * CW / kThreads;   // vectors of a slab per thread
   constexpr int PT = kThreads / CW;                  // pages one round of the block's threads covers
   static_assert(U >= 1 && U * PT == LVQ_MOVE_SLAB, "slab mapping");
@@ -109,27 +109,32 @@ __global__ void __launch_bounds__(kThreads) compact_pages_kernel(Geo g, int n_mo
   const size_t vpp = g.page_bytes / 16;
   const int p0 = tid / CW;
 
-  int2 mv[U];
-  uint4 v[U];
-  auto load = [&](int s0, int2 (&m)[U], uint4 (&x)[U]) {
+  // the moves are fetched two slabs ahead, the pages one
+  int2 mv[U], mn[U], mf[U];
+  uint4 v[U], vn[U];
+  auto fetch = [&](int s0, int2 (&m)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = s0 + p0 + u * PT;
       m[u] = i < n_moves ? __ldg(moves + i) : make_int2(-2, -2);
-      const bool skip = (m[u].x != LVQ_PAGE_HOLD && !in_pool(g, m[u].x)) || (m[u].y != LVQ_PAGE_HOLD && !in_pool(g, m[u].y));
-      if (skip) {
-        if (i < n_moves) set_status(st, LVQ_ECAPACITY);
+    }
+  };
+  auto load = [&](int s0, int2 (&m)[U], uint4 (&x)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if ((m[u].x != LVQ_PAGE_HOLD && !in_pool(g, m[u].x)) || (m[u].y != LVQ_PAGE_HOLD && !in_pool(g, m[u].y))) {
+        if (s0 + p0 + u * PT < n_moves) set_status(st, LVQ_ECAPACITY);
         m[u] = make_int2(-2, -2);
       }
       if (m[u].x >= 0) x[u] = load16(base + (size_t)m[u].x * vpp);
     }
   };
+  fetch(0, mv);
+  fetch(LVQ_MOVE_SLAB, mn);
   load(0, mv, v);
   for (int s0 = 0; s0 < n_moves; s0 += LVQ_MOVE_SLAB) {
-    int2 mn[U];
-    uint4 vn[U];
-    const bool more = s0 + LVQ_MOVE_SLAB < n_moves;
-    if (more) load(s0 + LVQ_MOVE_SLAB, mn, vn);
+    fetch(s0 + 2 * LVQ_MOVE_SLAB, mf);
+    load(s0 + LVQ_MOVE_SLAB, mn, vn);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (mv[u].x == LVQ_PAGE_HOLD) v[u] = hold[col];
@@ -140,10 +145,8 @@ __global__ void __launch_bounds__(kThreads) compact_pages_kernel(Geo g, int n_mo
       if (mv[u].y == LVQ_PAGE_HOLD) hold[col] = v[u];
     }
     __syncthreads();
-    if (more) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) { mv[u] = mn[u]; v[u] = vn[u]; }
-    }
+    for (int u = 0; u < U; ++u) { mv[u] = mn[u]; v[u] = vn[u]; mn[u] = mf[u]; }
   }
 }
 
@@ -151,9 +154,8 @@ cudaError_t launch_compact_pages(const Geo& g, int n_moves, const int32_t* moves
                                  uint8_t* idx, int32_t* st, int n_sm, cudaStream_t s) {
   const long long streams = (long long)g.L * g.nblk * g.H * 2;
   const int vpp = g.page_bytes / 16;
-  // few streams: a page's columns are spread over more CTAs, down to 32-byte pieces (one sector)
-  int cw = vpp < 8 ? vpp : 8;
-  while (cw > 2 && streams * (vpp / cw) < 2 * n_sm) cw /= 2;
+  // few streams: a page's columns are spread over more CTAs, down to 64-byte pieces
+  const int cw = vpp >= 8 && streams * (vpp / 8) >= 2 * n_sm ? 8 : 4;
   const long long move_ctas = n_moves > 0 ? streams * (vpp / cw) : 0;
   const long long entries = (long long)g.B * g.pts;
   const long long table_ctas = (entries + kTile - 1) / kTile < 1024 ? (entries + kTile - 1) / kTile : 1024;
@@ -161,8 +163,7 @@ cudaError_t launch_compact_pages(const Geo& g, int n_moves, const int32_t* moves
   const unsigned grid = (unsigned)(move_ctas + table_ctas);
   const int2* mv = reinterpret_cast<const int2*>(moves);
   if (cw == 8) compact_pages_kernel<8><<<grid, kThreads, 0, s>>>(g, n_moves, (int)move_ctas, mv, new_id, table, idx, st);
-  else if (cw == 4) compact_pages_kernel<4><<<grid, kThreads, 0, s>>>(g, n_moves, (int)move_ctas, mv, new_id, table, idx, st);
-  else compact_pages_kernel<2><<<grid, kThreads, 0, s>>>(g, n_moves, (int)move_ctas, mv, new_id, table, idx, st);
+  else compact_pages_kernel<4><<<grid, kThreads, 0, s>>>(g, n_moves, (int)move_ctas, mv, new_id, table, idx, st);
   return cudaGetLastError();
 }
 

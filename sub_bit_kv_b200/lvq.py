@@ -7,7 +7,9 @@ fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -360,19 +362,29 @@ class CompactionPlan:
         self.n_pages = int(n_pages)
         # one buffer, so that it goes to the device in one copy: the moves, then new_id
         self._room = 2 * (n + n // 2)
-        pin = torch.cuda.is_available()
-        self._host = torch.empty(self._room + max(1, self.n_pages), dtype=torch.int32, pin_memory=pin)
+        self._host = torch.empty(self._room + max(1, self.n_pages), dtype=torch.int32, pin_memory=_has_cuda())
         k = _I32()
         base = self._host.data_ptr()
         _check(lib().lvq_plan_compaction(self.n_pages, order.data_ptr() if n else None, n, base + 4 * self._room,
                                          base if n else None, ctypes.byref(k)), "lvq_plan_compaction")
         self.n_moves = k.value
-        self.moves = self._host[:2 * k.value].view(-1, 2)
-        self.new_id = self._host[self._room:]
+
+    @property
+    def moves(self) -> torch.Tensor:
+        return self._host[:2 * self.n_moves].view(-1, 2)
+
+    @property
+    def new_id(self) -> torch.Tensor:
+        return self._host[self._room:]
 
     @property
     def n_live(self) -> int:
         return int((self.new_id >= 0).sum())
+
+
+@functools.lru_cache(None)
+def _has_cuda() -> bool:
+    return torch.cuda.is_available()
 
 
 def lvq_plan_compaction(n_pages, order) -> CompactionPlan:
@@ -388,11 +400,12 @@ def lvq_compact_pages(cfg, lay, plan: CompactionPlan, page_table, idx, dev_statu
     dev, raw = torch.cuda.current_device(), _stream(stream)
     table, codes = _table(cfg, lay, dev, page_table), _on(dev, idx, "idx", torch.uint8, lay.idx_bytes)
     status = _on(dev, dev_status, "dev_status", torch.int32, 4)
-    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=dev) if stream is not None else None):
-        plan_dev = plan._host.to(torch.device("cuda", dev), non_blocking=True)
-        _check(lib().lvq_compact_pages(
-            ctypes.byref(cfg), ctypes.byref(lay), plan.n_moves, plan_dev.data_ptr(),
-            plan_dev.data_ptr() + 4 * plan._room, table, codes, status, raw), "lvq_compact_pages")
+    side = torch.cuda.stream(torch.cuda.ExternalStream(raw, device=dev)) if stream is not None else contextlib.nullcontext()
+    with side:                                  # (the plan's device copy belongs to the call's stream)
+        on_device = plan._host.cuda(non_blocking=True)
+        base = on_device.data_ptr()
+        _check(lib().lvq_compact_pages(ctypes.byref(cfg), ctypes.byref(lay), plan.n_moves, base, base + 4 * plan._room,
+                                       table, codes, status, raw), "lvq_compact_pages")
 
 
 def lvq_fork_requests(cfg, lay, parent, children, coded_tokens, tail_pages, ctx_len, coded_len, sink, ring, idx,

@@ -39,12 +39,12 @@ def test_shared_pages_are_free_with_their_last_holder():
 
 
 def _carry_out(plan, pages):
-    """The moves of a plan as lvq_compact_pages documents them: slabs of 128 pairs, the reads of a slab before
+    """The moves of a plan as lvq_compact_pages documents them: slabs of 64 pairs, the reads of a slab before
     its writes, -1 a page's worth of memory."""
     hold = None
     moves = plan.moves.tolist()
-    for s in range(0, len(moves), 128):
-        slab = moves[s:s + 128]
+    for s in range(0, len(moves), 64):
+        slab = moves[s:s + 64]
         values = [hold if src == -1 else pages[src] for src, _ in slab]
         for (_, dst), v in zip(slab, values):
             assert v is not None
@@ -69,7 +69,7 @@ def test_compaction_plan(n, live, seed):
 
 def test_compaction_plan_of_cycles():
     """Cycles shorter than a slab, as long, longer, and back to back."""
-    sizes = [2, 3, 126, 127, 128, 129, 300, 2, 500, 1, 128]
+    sizes = [2, 3, 62, 63, 64, 65, 126, 127, 128, 129, 300, 2, 500, 1, 128]
     order, at = [], 0
     for k in sizes:
         order += [at + (i + 1) % k for i in range(k)]
