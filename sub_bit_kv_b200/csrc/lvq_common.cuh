@@ -198,7 +198,7 @@ constexpr int kForkMax = 256;           // children one lvq_fork_requests call c
 cudaError_t launch_fork(const Geo& g, int parent, int n, const int32_t* children, int coded, const int32_t* tails,
                         int32_t* ctx_len, int32_t* coded_len, __nv_bfloat16* sink, __nv_bfloat16* ring, uint8_t* idx,
                         int32_t* table, int32_t* st, cudaStream_t s);
-constexpr int kSharedMaxBatch = 512;    // requests one lvq_decode_attention_shared call can take
+constexpr int kSharedMaxBatch = 256;    // requests one lvq_decode_attention_shared call can take
 cudaError_t launch_decode_shared(const Geo& g, int layer, int step, int batch, const __nv_bfloat16* q,
                                  const int32_t* ctx_len, const int32_t* coded_len, int n_groups,
                                  const int32_t* group_begin, const int32_t* group_tokens, const __nv_bfloat16* sink,

@@ -28,7 +28,7 @@ constexpr int kQT = 16;                 // query rows of a tile of shared tokens
 constexpr int kOT = 8;                  // query heads of a tile of own tokens
 constexpr int kTT = 16;                 // tokens of a tile: two pages
 constexpr int kSharedCost = 20;         // fixed cost of a query tile of a shared entry, in token tiles
-constexpr int kOwnCost = 3;             // the same of an own entry
+constexpr int kOwnCost = 8;             // the same of an own entry
 constexpr int kWarps = 8;
 constexpr int kShThreads = 32 * kWarps;
 constexpr float kNoMax = -1e30f;        // softmax reference before the first token
@@ -46,118 +46,126 @@ struct SharedArgs {
   int32_t* st;
 };
 
-// Counters of the batch in shared memory (the partition's inputs).
+// Counters of the batch in shared memory, and the partition's running costs.
 struct Counters {
+  long long *gcum, *ocum;               // [ng + 1], [batch + 1]: cost of the shared (own) entries before each
   int *ctx, *coded, *own0;              // [batch]: context (0: unusable), coded tokens, shared tokens of its group
   int *gb, *sh, *lead;                  // [ng + 1], [ng], [ng]: first request, shared tokens, first usable request
 };
+constexpr int counter_bytes(int batch, int ng) { return 8 * (ng + batch + 2) + 4 * (3 * batch + 3 * ng + 1); }
 
 __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Entries 0 .. ng-1: the groups' shared tokens; ng .. ng+batch-1: the requests' own tokens.
+// Token tiles, query tiles and fixed cost of a query tile.
 struct Entry {
-  int tiles, qtiles, fixed;             // token tiles, query tiles, fixed cost of a query tile
+  int tiles, qtiles, fixed;
   __device__ long long each() const { return fixed + tiles; }
   __device__ long long cost() const { return tiles ? qtiles * each() : 0; }
 };
-__device__ inline Entry entry_of(const Geo& g, const Counters& c, int ng, int e) {
-  const int rep = g.Hq / g.H;
-  if (e < ng) return {ceil_div(c.sh[e], kTT), ceil_div((c.gb[e + 1] - c.gb[e]) * rep, kQT), kSharedCost};
-  const int b = e - ng, ctx = c.ctx[b], rest = c.coded[b] - c.own0[b];
-  return {ceil_div(rest, kTT) + ceil_div(ctx - c.coded[b], kTT), ceil_div(rep, kOT), kOwnCost};
+__device__ inline Entry shared_entry(const Geo& g, const Counters& c, int i) {
+  return {ceil_div(c.sh[i], kTT), ceil_div((c.gb[i + 1] - c.gb[i]) * (g.Hq / g.H), kQT), kSharedCost};
+}
+__device__ inline Entry own_entry(const Geo& g, const Counters& c, int b) {
+  return {ceil_div(c.coded[b] - c.own0[b], kTT) + ceil_div(c.ctx[b] - c.coded[b], kTT), ceil_div(g.Hq / g.H, kOT), kOwnCost};
 }
 
-// The entry of [e0, e1) in which cost `x` lies (counted from e0's start) and the cost before it; one
-// warp, the entries summed lane by lane.  e1 if x is not below the total, which *total receives.
-__device__ inline int locate(const Geo& g, const Counters& c, int ng, int e0, int e1, long long x, long long* before,
-                             long long* total) {
-  const int lane = threadIdx.x & 31, per = ceil_div(e1 - e0, 32);
-  long long mine = 0;
-  for (int i = lane * per; i < min(e1 - e0, (lane + 1) * per); ++i) mine += entry_of(g, c, ng, e0 + i).cost();
+// The entry of [0, n) in which cost x lies, n if x is not below the total.
+__device__ inline int locate(const long long* cum, int n, long long x) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (cum[mid + 1] > x) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// cum[i + 1] = the sum of the threads' costs 0 .. i (thread i < n: entry i).  `part`: a value per warp.
+__device__ inline void scan_costs(long long mine, int n, long long* cum, long long* part) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long up = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long v = __shfl_up_sync(0xffffffffu, up, o);
     if (lane >= o) up += v;
   }
-  *total = __shfl_sync(0xffffffffu, up, 31);
-  const unsigned in = __ballot_sync(0xffffffffu, up > x);
-  if (in == 0) {
-    *before = *total;
-    return e1;
-  }
-  const int first = __ffs(in) - 1;
-  long long at = __shfl_sync(0xffffffffu, up - mine, first);
-  int e = e0 + first * per;
-  for (;; ++e) {
-    const long long cost = entry_of(g, c, ng, e).cost();
-    if (at + cost > x) break;
-    at += cost;
-  }
-  *before = at;
-  return e;
+  if (lane == 31) part[warp] = up;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) up += part[w];
+  if (tid < n) cum[tid + 1] = up;
+  if (tid == 0) cum[0] = 0;
 }
 
-// Loads and checks the counters; returns false (for every thread) if group_begin is not as described.
-__device__ bool load_counters(const Geo& g, const SharedArgs& a, Counters& c, bool report) {
-  const int tid = threadIdx.x;
+// Loads and checks the counters and derives the costs, a thread to a request and to a group; returns false (for
+// every thread) if group_begin is not as described.
+__device__ bool load_counters(const Geo& g, const SharedArgs& a, Counters& c, long long* part, bool report) {
+  static_assert(kSharedMaxBatch <= kShThreads, "a thread to a request");
+  const int t = threadIdx.x;
   bool ok = true;
-  for (int i = tid; i <= a.ng; i += kShThreads) {
-    const int v = __ldcg(a.gb + i);
-    c.gb[i] = v;
-    ok = ok && v >= 0 && v <= a.batch && (i > 0 || v == 0) && (i < a.ng || v == a.batch);
-    if (i < a.ng) {
-      ok = ok && __ldcg(a.gb + i + 1) >= v;
-      c.sh[i] = max(0, __ldcg(a.gt + i)) / kPage * kPage;
-      c.lead[i] = a.batch;
-    }
+  int ctx = 0, L = 0, v = 0, next = 0, tokens = 0;
+  if (t < a.batch) { ctx = __ldcg(a.ctx_len + t); L = __ldcg(a.coded_len + t); }
+  if (t < a.ng) { v = __ldcg(a.gb + t); next = __ldcg(a.gb + t + 1); tokens = __ldcg(a.gt + t); }
+  if (t < a.ng) {
+    ok = v >= 0 && next >= v && next <= a.batch && (t > 0 || v == 0) && (t < a.ng - 1 || next == a.batch);
+    c.gb[t] = v;
+    if (t == a.ng - 1) c.gb[a.ng] = next;
+    c.sh[t] = max(0, tokens) / kPage * kPage;
+    c.lead[t] = a.batch;
   }
-  for (int b = tid; b < a.batch; b += kShThreads) {
-    const int ctx = __ldcg(a.ctx_len + b), L = __ldcg(a.coded_len + b);
+  if (t < a.batch) {
     const int recent = ctx - min(g.S, max(ctx, 0)) - L;
-    const bool bad = ctx < 1 || ctx > g.max_ctx || L < 0 || L > g.P * kPage || (L > 0 && ctx < g.S + L) || recent < 0 ||
-                     recent > g.R;
-    if (bad && report) set_status(a.st, LVQ_ECAPACITY);
-    c.ctx[b] = bad ? 0 : ctx;
-    c.coded[b] = bad ? 0 : L;
+    const bool bad = ctx < 1 || ctx > g.max_ctx || L < 0 || L > g.P * kPage || (L > 0 && ctx < g.S + L) || recent < 0 || recent > g.R;
+    if (bad) {
+      if (report) set_status(a.st, LVQ_ECAPACITY);
+      ctx = L = 0;
+    }
+    c.ctx[t] = ctx;
+    c.coded[t] = L;
   }
   if (__syncthreads_or(!ok)) {
-    if (tid == 0 && report) set_status(a.st, LVQ_EINVAL);
+    if (t == 0 && report) set_status(a.st, LVQ_EINVAL);
     return false;
   }
   // a group shares no more than its shortest usable request has coded
-  auto group_of = [&](int b) {
-    int lo = 0, hi = a.ng;                       // the last group that begins at or before b
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (c.gb[mid] <= b) lo = mid; else hi = mid;
+  int grp = 0;
+  if (t < a.batch) {
+    int hi = a.ng;                               // the last group that begins at or before the request
+    while (hi - grp > 1) {
+      const int mid = (grp + hi) / 2;
+      if (c.gb[mid] <= t) grp = mid; else hi = mid;
     }
-    return lo;
-  };
-  for (int b = tid; b < a.batch; b += kShThreads)
-    if (c.ctx[b] > 0) {
-      atomicMin(&c.sh[group_of(b)], c.coded[b] / kPage * kPage);
-      atomicMin(&c.lead[group_of(b)], b);
+    if (ctx > 0) {
+      atomicMin(&c.sh[grp], L / kPage * kPage);
+      atomicMin(&c.lead[grp], t);
     }
+  }
   __syncthreads();
-  for (int b = tid; b < a.batch; b += kShThreads) c.own0[b] = c.ctx[b] > 0 ? c.sh[group_of(b)] : 0;
-  for (int e = tid; e < a.ng; e += kShThreads)
-    if (c.lead[e] == a.batch) c.sh[e] = 0;       // no usable request
+  if (t < a.ng && c.lead[t] == a.batch) c.sh[t] = 0;   // no usable request
+  if (t < a.batch) c.own0[t] = ctx > 0 ? c.sh[grp] : 0;
+  scan_costs(t < a.ng ? shared_entry(g, c, t).cost() : 0, a.ng, c.gcum, part);
+  __syncthreads();
+  scan_costs(t < a.batch ? own_entry(g, c, t).cost() : 0, a.batch, c.ocum, part);
   __syncthreads();
   return true;
 }
 
 // Pool mode: the rows of a group name the same pages for its shared tokens.  The CTAs share the comparison.
 __device__ void check_rows(const Geo& g, const SharedArgs& a, const Counters& c) {
-  const int n_thr = gridDim.x * gridDim.y * kShThreads, me = (blockIdx.y * gridDim.x + blockIdx.x) * kShThreads + threadIdx.x;
-  bool ok = true;
-  for (int e = 0; e < a.ng; ++e)
-    for (int b = c.lead[e] + 1; b < c.gb[e + 1]; ++b) {
-      if (c.ctx[b] == 0) continue;
-      const int32_t *x = g.pt + (size_t)c.lead[e] * g.pts, *y = g.pt + (size_t)b * g.pts;
-      for (int p = me; p < c.sh[e] / kPage; p += n_thr) ok = ok && __ldg(x + p) == __ldg(y + p);
+  const int n_cta = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
+  bool differ = false;
+  for (int e = 0; e < a.ng; ++e) {
+    const int pages = c.sh[e] / kPage, first = c.lead[e], others = c.gb[e + 1] - first - 1;
+    if (pages == 0 || others < 1) continue;
+    // this CTA's pages of the group's list, against the rows of all its other requests
+    const int p0 = (int)((long long)pages * me / n_cta), n = (int)((long long)pages * (me + 1) / n_cta) - p0;
+    const int32_t* lead_row = g.pt + (size_t)first * g.pts + p0;
+    const int total = n * others;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < total; i += kShThreads) {
+      const int b = first + 1 + i / n, p = i % n;
+      if (c.ctx[b] > 0) differ |= __ldcg(lead_row + p) != __ldcg(g.pt + (size_t)b * g.pts + p0 + p);
     }
-  if (!ok) set_status(a.st, LVQ_EINVAL);
+  }
+  if (differ) set_status(a.st, LVQ_EINVAL);
 }
 
 // A query tile of an entry: rows r < nrows are (request, query head) pairs.
@@ -186,19 +194,21 @@ struct Sh {
   static constexpr int NST = PARK / STAGE < 6 ? PARK / STAGE : 6;
   static constexpr int OFF_V = KS;
   static constexpr int OFF_W = OFF_V + kEntries * VROW;
-  static constexpr int OFF_F = OFF_W + kWarps * WARP;
+  static constexpr int OFF_Q = OFF_W + kWarps * WARP;
+  static constexpr int OFF_F = OFF_Q + 2 * NW * 32 * 16;
   static constexpr int OFF_R = OFF_F + NW * 32 * 16;
   static constexpr int OFF_ML = OFF_R + kWarps * F * 8;
   static constexpr int OFF_INV = OFF_ML + kWarps * kQT * 8;
   static constexpr int OFF_RED = OFF_INV + kQT * 4;
   static constexpr int OFF_BAR = OFF_RED + 4 * kWarps * 4;
-  static constexpr int OFF_C = OFF_BAR + 16;
-  static constexpr int smem(int batch, int ng) { return OFF_C + (3 * batch + 3 * ng + 1) * 4; }
+  static constexpr int OFF_P = OFF_BAR + 16;
+  static constexpr int OFF_C = OFF_P + kWarps * 8;
+  static constexpr int smem(int batch, int ng) { return OFF_C + counter_bytes(batch, ng); }
   static_assert(NP % 4 == 0 && NI * C == 2 * NW, "lane mapping");
   static_assert(NST >= 3 && NST <= 8, "stages (a tile's RoPE row is read before the one 8 tiles on is fetched)");
-  static_assert(kWarps * WARP >= KS && WARP >= 2 * NW * 32 * 16 && PARK >= NW * 32 * 16, "the warps' areas");
-  static_assert(OFF_C + (6 * kSharedMaxBatch + 1) * 4 <= 227 * 1024, "shared memory");
-  static_assert(OFF_W % 16 == 0 && PARK % 16 == 0 && OFF_F % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+  static_assert(kWarps * WARP >= KS && PARK >= NW * 32 * 16, "the warps' areas");
+  static_assert(OFF_C + counter_bytes(kSharedMaxBatch, kSharedMaxBatch) <= 227 * 1024, "shared memory");
+  static_assert(OFF_W % 16 == 0 && PARK % 16 == 0 && OFF_F % 16 == 0 && OFF_BAR % 8 == 0 && OFF_C % 8 == 0, "alignment");
 };
 
 __device__ inline uint32_t pack_h2(float lo, float hi) {
@@ -678,7 +688,9 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   uint32_t* red = reinterpret_cast<uint32_t*>(sm + X::OFF_RED);
   const uint32_t bar = smem_addr(sm + X::OFF_BAR);
   Counters c;
-  c.ctx = reinterpret_cast<int*>(sm + X::OFF_C);
+  c.gcum = reinterpret_cast<long long*>(sm + X::OFF_C);
+  c.ocum = c.gcum + a.ng + 1;
+  c.ctx = reinterpret_cast<int*>(c.ocum + a.batch + 1);
   c.coded = c.ctx + a.batch; c.own0 = c.coded + a.batch; c.gb = c.own0 + a.batch; c.sh = c.gb + a.ng + 1; c.lead = c.sh + a.ng;
   const __nv_bfloat16* kslice = a.cbp + cbp_slice_off(g, a.layer, 0, blk, h, step_s);
   const __nv_bfloat16* vslice = a.cbp + cbp_slice_off(g, a.layer, 1, blk, h, step_s);
@@ -698,7 +710,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
     bulk_g2s(smem_addr(Ks), kslice, X::KS, bar);
     bulk_g2s(smem_addr(sm + X::OFF_W), vslice, X::KS, bar);
   }
-  const bool ok = load_counters(g, a, c, j == 0 && h == 0);   // (its barriers publish the mbarrier)
+  const bool ok = load_counters(g, a, c, reinterpret_cast<long long*>(sm + X::OFF_P), j == 0 && h == 0);   // (its barriers publish the mbarrier)
   // every slot of this part starts empty
   for (int i = tid; i < a.batch * rep * 2; i += kShThreads) {
     const int b = i / (rep * 2), r = i / 2 % rep;
@@ -720,17 +732,60 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
     bk.ec[w] = make_float2(x.x, x.z);
     bk.es[w] = make_float2(x.y, x.w);
   }
-  if (ok && g.pool) check_rows(g, a, c);
-  // this part of the head's list: [cut0, cut1), shared entries first
-  long long shared_total = 0, own_total = 0, before = 0, own_before = 0;
-  int e0 = 0;
+  const float qk_scale = 1.4426950408889634f / sqrtf((float)D);
+  // Fragments of a query tile: D / 4 lanes rotate a row at its own position, scale it to fp16's range and split it.
+  auto set_queries = [&](const RowTile& rt) {
+    uint4* Qf = reinterpret_cast<uint4*>(sm + X::OFF_Q);       // [hi, lo][k step][lane]
+    constexpr int LPR = D / 4, RPW = 32 / LPR;                 // lanes of a row, rows a warp takes at once
+    const int f2 = lane % LPR, P = 2 * f2 / C, sub = 2 * f2 % C / 2;
+#pragma unroll 2
+    for (int r = warp * RPW + lane / LPR; r < kQT; r += kWarps * RPW) {
+      const bool live = r < rt.nrows && c.ctx[rt.request(r)] > 0;
+      float2 x, y;
+      float inv;
+      query_pair<D>(g, a, live ? a.q + ((size_t)rt.request(r) * g.Hq + rt.head(r)) * D : a.q, live ? c.ctx[rt.request(r)] - 1 : 0, f2,
+                    qk_scale, live, x, y, &inv);
+      uint32_t xh, xl, yh, yl;
+      split_h2(x, xh, xl);
+      split_h2(y, yh, yl);
+      const int ks = P / 4 * (C / 2) + sub, fl = (r & 7) * 4 + P % 4, rg = r >> 3;
+      uint32_t* fh = reinterpret_cast<uint32_t*>(Qf + ks * 32 + fl);
+      uint32_t* fw = reinterpret_cast<uint32_t*>(Qf + (X::NW + ks) * 32 + fl);
+      fh[rg] = xh; fh[rg + 2] = yh;
+      fw[rg] = xl; fw[rg + 2] = yl;
+      if (f2 == 0) inv_s[r] = inv;
+    }
+  };
+  // this part of the head's list: [cut0, cut1), shared entries first; e, qt: where it begins
+  const long long shared_total = ok ? c.gcum[a.ng] : 0, total = ok ? shared_total + c.ocum[a.batch] : 0;
+  const long long cut0 = total * j / a.k, cut1 = total * (j + 1) / a.k;
+  int e = a.ng, qt = 0;
+  Entry en = {0, 0, 0};
+  RowTile rt;
+  rt.rep = rep; rt.h = h;
+  auto next_tile = [&](bool first) {                           // moves on to the part's next query tile of shared tokens
+    if (first) e = locate(c.gcum, a.ng, cut0);
+    for (;; ++e, first = true) {
+      if (e >= a.ng || c.gcum[e] >= cut1) { e = a.ng; return; }
+      en = shared_entry(g, c, e);
+      if (en.tiles == 0) continue;
+      for (qt = first ? (cut0 > c.gcum[e] ? (int)((cut0 - c.gcum[e]) / en.each()) : 0) : qt + 1; qt < en.qtiles; ++qt) {
+        const long long base = c.gcum[e] + qt * en.each() + en.fixed;
+        if (base >= cut1) { e = a.ng; return; }
+        if (max(0ll, cut0 - base) < min((long long)en.tiles, cut1 - base)) {
+          rt.b0 = c.gb[e];
+          rt.r0 = qt * kQT;
+          rt.nrows = min(kQT, (c.gb[e + 1] - c.gb[e]) * rep - rt.r0);
+          return;
+        }
+      }
+    }
+  };
   if (ok) {
-    locate(g, c, a.ng, a.ng, a.ng + a.batch, 0, &own_before, &own_total);
-    locate(g, c, a.ng, 0, a.ng, 0, &before, &shared_total);
+    next_tile(true);
+    if (e < a.ng) set_queries(rt);
+    if (g.pool) check_rows(g, a, c);
   }
-  const long long cut0 = (shared_total + own_total) * j / a.k, cut1 = (shared_total + own_total) * (j + 1) / a.k;
-  if (ok) e0 = locate(g, c, a.ng, 0, a.ng, cut0, &before, &shared_total);
-
   const bool late = __syncthreads_or(!mbar_wait(bar, 0, g.wait_iters));
   if (late || !ok) {
     if (late && tid == 0) {
@@ -751,12 +806,16 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
       w &= 0x7fff7fffu;
       return ((w & 0xffffu) < 0x7f80u ? w & 0xffffu : 0u) | ((w >> 16) < 0x7f80u ? w & 0xffff0000u : 0u);
     };
+    constexpr int NV = X::KS / 16 / kShThreads;
     uint32_t ka = 0, va = 0;
-#pragma unroll 4
-    for (int i = tid; i < X::KS / 16; i += kShThreads) {
-      ka = amax(kw[i], ka);
-      va = amax(vw[i], va);
+    uint4 v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v[i] = vw[tid + i * kShThreads];
+      va = amax(v[i], va);
     }
+#pragma unroll 4
+    for (int i = 0; i < NV; ++i) ka = amax(kw[tid + i * kShThreads], ka);
     ka = max(ka & 0xffffu, ka >> 16);
     va = max(va & 0xffffu, va >> 16);
     if (__any_sync(0xffffffffu, max(ka, va) >= 0x7f80u)) {     // infinities or NaN among the entries: they count nothing
@@ -776,67 +835,33 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
     bk.ks = pow2i(fit_exp(ka));
     bk.kinv = pow2i(-fit_exp(ka));
     const float vscale = pow2i(fit_exp(va) + 1);
-#pragma unroll 4
-    for (int i = tid; i < X::KS / 16; i += kShThreads) {
-      const uint4 w = vw[i];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int at = tid + i * kShThreads;
       auto cv = [&](uint32_t x) { return pack_h2(bf16_lo(x) * vscale, bf16_hi(x) * vscale); };
-      *reinterpret_cast<uint4*>(Vs + (i / (D / 8)) * X::VROW + (i % (D / 8)) * 16) = make_uint4(cv(w.x), cv(w.y), cv(w.z), cv(w.w));
+      *reinterpret_cast<uint4*>(Vs + (at / (D / 8)) * X::VROW + (at % (D / 8)) * 16) =
+          make_uint4(cv(v[i].x), cv(v[i].y), cv(v[i].z), cv(v[i].w));
     }
     if (tid == 0) red[2 * kWarps] = __float_as_uint(pow2i(-fit_exp(va) - 1));
     __syncthreads();
   }
   const float vback = __uint_as_float(red[2 * kWarps]);
-  const float qk_scale = 1.4426950408889634f / sqrtf((float)D);
   auto slot_of = [&](int b, int hq, int kind) { return (((size_t)b * g.Hq + hq) * g.max_splits + j) * 2 + kind; };
 
   // ---- shared entries: the CTA's warps share out the tiles of one query tile at a time
-  long long at = before;
-  for (int e = e0; e < a.ng && at < cut1; ++e) {
-    const Entry en = entry_of(g, c, a.ng, e);
-    if (en.tiles == 0) continue;
-    const long long at0 = at;
-    at += en.cost();
-    for (int qt = cut0 > at0 ? (int)min((long long)en.qtiles, (cut0 - at0) / en.each()) : 0; qt < en.qtiles; ++qt) {
-      const long long base = at0 + qt * en.each() + en.fixed;
-      if (base >= cut1) break;
+  while (e < a.ng) {
+    {
+      const long long base = c.gcum[e] + qt * en.each() + en.fixed;
       const int t0 = (int)max(0ll, cut0 - base), t1 = (int)min((long long)en.tiles, cut1 - base);
-      if (t0 >= t1) continue;
-      RowTile rt;
-      rt.b0 = c.gb[e];
-      rt.rep = rep; rt.r0 = qt * kQT; rt.h = h;
-      rt.nrows = min(kQT, (c.gb[e + 1] - c.gb[e]) * rep - rt.r0);
-      {
-        uint4* Qf = reinterpret_cast<uint4*>(sm + X::OFF_W);   // [hi, lo][k step][lane], in the first warps' areas
-        constexpr int LPR = D / 4, RPW = 32 / LPR;             // lanes of a row, rows a warp takes at once
-        const int f2 = lane % LPR, P = 2 * f2 / C, sub = 2 * f2 % C / 2;
-        for (int r = warp * RPW + lane / LPR; r < kQT; r += kWarps * RPW) {
-          const bool live = r < rt.nrows && c.ctx[rt.request(r)] > 0;
-          float2 x, y;
-          float inv;
-          query_pair<D>(g, a, live ? a.q + ((size_t)rt.request(r) * g.Hq + rt.head(r)) * D : a.q, live ? c.ctx[rt.request(r)] - 1 : 0, f2,
-                        qk_scale, live, x, y, &inv);
-          uint32_t xh, xl, yh, yl;
-          split_h2(x, xh, xl);
-          split_h2(y, yh, yl);
-          const int ks = P / 4 * (C / 2) + sub, fl = (r & 7) * 4 + P % 4, rg = r >> 3;
-          uint32_t* fh = reinterpret_cast<uint32_t*>(Qf + ks * 32 + fl);
-          uint32_t* fw = reinterpret_cast<uint32_t*>(Qf + (X::NW + ks) * 32 + fl);
-          fh[rg] = xh; fh[rg + 2] = yh;
-          fw[rg] = xl; fw[rg + 2] = yl;
-          if (f2 == 0) inv_s[r] = inv;
-        }
-      }
-      __syncthreads();
       uint32_t qf[2][X::NW][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int w = 0; w < X::NW; ++w) {
-          const uint4 u = reinterpret_cast<const uint4*>(sm + X::OFF_W)[(i * X::NW + w) * 32 + lane];
+          const uint4 u = reinterpret_cast<const uint4*>(sm + X::OFF_Q)[(i * X::NW + w) * 32 + lane];
           qf[i][w][0] = u.x; qf[i][w][1] = u.y; qf[i][w][2] = u.z; qf[i][w][3] = u.w;
         }
       const float qinv[2] = {inv_s[row], inv_s[row + 8]};
-      __syncthreads();                                         // the fragments are read
       State<D, C> st;
       st.clear();
       const int w0 = t0 + (int)((long long)(t1 - t0) * warp / kWarps), w1 = t0 + (int)((long long)(t1 - t0) * (warp + 1) / kWarps);
@@ -887,6 +912,8 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
           if (c0 == 0) a.pml[slot] = make_float2(M, L);
         }
       }
+      next_tile(false);
+      if (e < a.ng) set_queries(rt);                           // (every warp is past reading the last ones)
       __syncthreads();
     }
   }
@@ -900,12 +927,10 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   int park = -1, open = -1, open_b = 0, open_qt = 0, ended = 0, any = 0;   // open: the last piece, which other warps continue
   __syncthreads();                                             // (red is reused)
   if (x0 < x1) {
-    int e = locate(g, c, a.ng, a.ng, a.ng + a.batch, x0, &own_before, &own_total);
-    long long eat = own_before;
-    for (; e < a.ng + a.batch && eat < x1; ++e) {
-      const Entry en = entry_of(g, c, a.ng, e);
+    for (int b = locate(c.ocum, a.batch, x0); b < a.batch && c.ocum[b] < x1; ++b) {
+      const Entry en = own_entry(g, c, b);
       if (en.tiles == 0) continue;
-      const int b = e - a.ng;
+      const long long eat = c.ocum[b];
       for (int qt = x0 > eat ? (int)min((long long)en.qtiles, (x0 - eat) / en.each()) : 0; qt < en.qtiles; ++qt) {
         const long long base = eat + qt * en.each() + en.fixed;
         if (base >= x1) break;
@@ -995,7 +1020,6 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
         }
         __syncwarp();
       }
-      eat += en.cost();
     }
   }
   if (lane == 0) {

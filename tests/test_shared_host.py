@@ -165,8 +165,8 @@ def test_shared_attention_checks_its_arguments():
     for kw in (dict(layer=2), dict(layer=-1), dict(step=4), dict(batch=5), dict(batch=-1), dict(q=None), dict(q=FAKE + 8),
                dict(groups=0), dict(groups=5), dict(groups=-1), dict(gb=None), dict(sink=None), dict(ns=-1), dict(ns=65), dict(ws=None)):
         assert attend(**kw) == lvq.LVQ_EINVAL, kw
-    big = make_cfg(synth.WORKLOADS["tiny"], max_batch=600)
-    assert attend(batch=513, cfg=big, lay=lvq.lvq_cache_layout(big)) == lvq.LVQ_EUNSUPPORTED
+    big = make_cfg(synth.WORKLOADS["tiny"], max_batch=300)
+    assert attend(batch=257, cfg=big, lay=lvq.lvq_cache_layout(big)) == lvq.LVQ_EUNSUPPORTED
     if not torch.cuda.is_available():
         assert attend() == lvq.LVQ_EDEVICE
         assert attend(batch=0, groups=0, q=None) == lvq.LVQ_EDEVICE
