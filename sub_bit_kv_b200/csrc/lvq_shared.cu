@@ -28,7 +28,7 @@ constexpr int kQT = 16;                 // query rows of a tile of shared tokens
 constexpr int kOT = 8;                  // query heads of a tile of own tokens
 constexpr int kTT = 16;                 // tokens of a tile: two pages
 constexpr int kSharedCost = 20;         // fixed cost of a query tile of a shared entry, in token tiles
-constexpr int kOwnCost = 8;             // the same of an own entry
+constexpr int kOwnCost = 4;             // the same of an own entry
 constexpr int kWarps = 8;
 constexpr int kShThreads = 32 * kWarps;
 constexpr float kNoMax = -1e30f;        // softmax reference before the first token
@@ -55,18 +55,28 @@ struct Counters {
 constexpr int counter_bytes(int batch, int ng) { return 8 * (ng + batch + 2) + 4 * (3 * batch + 3 * ng + 1); }
 
 __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// a / b of non-negative costs: a 64-bit division takes some hundred instructions, and only absurd batches need one
+__device__ inline long long div_cost(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
 
 // Token tiles, query tiles and fixed cost of a query tile.
 struct Entry {
   int tiles, qtiles, fixed;
-  __device__ long long each() const { return fixed + tiles; }
+  int coded, weight;                    // own entries: tiles [0, coded) are coded, the others cost `weight` each
+  __device__ int units() const { return coded + (tiles - coded) * weight; }
+  __device__ int tile_at(int u) const { return u <= coded ? u : coded + ceil_div(u - coded, weight); }   // first one at or past unit u
+  __device__ long long each() const { return fixed + units(); }
   __device__ long long cost() const { return tiles ? qtiles * each() : 0; }
 };
 __device__ inline Entry shared_entry(const Geo& g, const Counters& c, int i) {
-  return {ceil_div(c.sh[i], kTT), ceil_div((c.gb[i + 1] - c.gb[i]) * (g.Hq / g.H), kQT), kSharedCost};
+  const int tiles = ceil_div(c.sh[i], kTT);
+  return {tiles, ceil_div((c.gb[i + 1] - c.gb[i]) * (g.Hq / g.H), kQT), kSharedCost, tiles, 1};
 }
 __device__ inline Entry own_entry(const Geo& g, const Counters& c, int b) {
-  return {ceil_div(c.coded[b] - c.own0[b], kTT) + ceil_div(c.ctx[b] - c.coded[b], kTT), ceil_div(g.Hq / g.H, kOT), kOwnCost};
+  const int rep = g.Hq / g.H, coded = ceil_div(c.coded[b] - c.own0[b], kTT);
+  // (a bf16 tile takes a warp 3100 cycles with one query head, like a coded one, and about a third more for each further)
+  return {coded + ceil_div(c.ctx[b] - c.coded[b], kTT), ceil_div(rep, kOT), kOwnCost, coded, (min(rep, kOT) + 2) / 3};
 }
 
 // The entry of [0, n) in which cost x lies, n if x is not below the total.
@@ -193,10 +203,11 @@ struct Sh {
   static constexpr int PARK = kOT * OROW * 4;
   static constexpr int NST = PARK / STAGE < 6 ? PARK / STAGE : 6;
   static constexpr int OFF_V = KS;
-  static constexpr int OFF_W = OFF_V + kEntries * VROW;
+  static constexpr int OFF_W = OFF_V + (kEntries * VROW + 15) / 16 * 16;
   static constexpr int OFF_Q = OFF_W + kWarps * WARP;
   static constexpr int OFF_F = OFF_Q + 2 * NW * 32 * 16;
-  static constexpr int OFF_R = OFF_F + NW * 32 * 16;
+  static constexpr int OFF_E = OFF_F + NW * 32 * 16;
+  static constexpr int OFF_R = OFF_E + NW * 4 * 16;
   static constexpr int OFF_ML = OFF_R + kWarps * F * 8;
   static constexpr int OFF_INV = OFF_ML + kWarps * kQT * 8;
   static constexpr int OFF_RED = OFF_INV + kQT * 4;
@@ -206,7 +217,7 @@ struct Sh {
   static constexpr int smem(int batch, int ng) { return OFF_C + counter_bytes(batch, ng); }
   static_assert(NP % 4 == 0 && NI * C == 2 * NW, "lane mapping");
   static_assert(NST >= 3 && NST <= 8, "stages (a tile's RoPE row is read before the one 8 tiles on is fetched)");
-  static_assert(kWarps * WARP >= KS && PARK >= NW * 32 * 16, "the warps' areas");
+  static_assert(PARK >= NW * 32 * 16, "the warps' areas");
   static_assert(OFF_C + counter_bytes(kSharedMaxBatch, kSharedMaxBatch) <= 227 * 1024, "shared memory");
   static_assert(OFF_W % 16 == 0 && PARK % 16 == 0 && OFF_F % 16 == 0 && OFF_BAR % 8 == 0 && OFF_C % 8 == 0, "alignment");
 };
@@ -292,7 +303,7 @@ template <int D, int C>
 struct Book {
   const unsigned char *Ks, *Vs;         // step slices: keys bf16, values scaled fp16 in padded rows
   const float4* Ff;                     // [frequency pair][lane]: (cos, cos, sin, sin) at (S % 8 + j)
-  float2 ec[Sh<D, C>::NW], es[Sh<D, C>::NW];   // the lane's e^{i 8 theta}
+  const float4* E8;                     // [frequency pair][quad]: e^{i 8 theta}, (cos, cos, sin, sin)
   float ks, kinv;                       // key scale (a power of two) and its reciprocal
 };
 
@@ -300,7 +311,43 @@ struct Book {
 struct Run {
   int lead, pg0, pg_end, n;
   const uint8_t *kcode, *vcode;         // code streams (pool mode: pools) of the head
+  int ids, ids_at;                      // physical pages [ids_at, ids_at + 32) of the run, one a lane
 };
+
+// Tile t's codes into its stage; every eighth tile's RoPE row (of its first page) as well.
+template <int D, int C>
+__device__ __forceinline__ void fetch_tile(const Geo& g, const SharedArgs& a, Run& run, int t, unsigned char* stages, float4* rrow) {
+  using X = Sh<D, C>;
+  const int lane = threadIdx.x & 31, pp = 2 * t;
+  if (pp - run.ids_at >= 32) {
+    run.ids_at = pp;
+    run.ids = phys_page(g, run.lead, min(run.pg0 + pp + lane, run.pg_end - 1));
+    if (run.ids < 0) {
+      set_status(a.st, LVQ_ECAPACITY);
+      run.ids = 0;
+    }
+  }
+  const int i0 = __shfl_sync(0xffffffffu, run.ids, pp - run.ids_at), i1 = __shfl_sync(0xffffffffu, run.ids, pp + 1 - run.ids_at);
+  const uint32_t dst = smem_addr(stages) + (t % X::NST) * X::STAGE;
+  constexpr int VP = X::PAGE / 16;
+#pragma unroll
+  for (int v = lane; v < 4 * VP; v += 32) {
+    const int id = (v / VP) & 1 ? i1 : i0;
+    cp_async16(dst + v * 16, (v < 2 * VP ? run.kcode : run.vcode) + (size_t)id * X::PAGE + v % VP * 16);
+  }
+  if (t % 8 == 0 && lane < X::F / 2)
+    cp_async16(smem_addr(rrow) + lane * 16,
+               reinterpret_cast<const float4*>(a.rope) + (size_t)(run.pg0 + pp + (g.S >> 3)) * (X::F / 2) + lane);
+}
+// The first tiles of a run are on their way: called as early as the pages are known, and once before coded_run.
+template <int D, int C>
+__device__ __forceinline__ void begin_run(const Geo& g, const SharedArgs& a, Run& run, unsigned char* stages, float4* rrow) {
+#pragma unroll
+  for (int t = 0; t < Sh<D, C>::NST - 1; ++t) {
+    if (t * kTT < run.n) fetch_tile<D, C>(g, a, run, t, stages, rrow);
+    cp_commit();
+  }
+}
 
 // o += weights x values of a tile.  The tensor core cuts its sums off towards zero, so a tile's product starts from
 // zero and is added in fp32, rounded to nearest: carried through a run's products the cut biases an output by
@@ -326,43 +373,21 @@ __device__ inline void add_values(float (&o)[4], const uint32_t (&ph)[4], const 
 // and queries enter as sums of two fp16 values, good to 2^-22 of the largest; lo x lo is left out of 16 rows.
 // Weights too are sums of two fp16 values; values are exact.
 template <int D, int C, bool STK>
-__device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, const Book<D, C>& bk, const Run& run, State<D, C>& st,
+__device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, const Book<D, C>& bk, Run& run, State<D, C>& st,
                                           const uint32_t (&qf)[STK ? 1 : 2][Sh<D, C>::NW][4], const float (&qinv)[2],
                                           unsigned char* stages, float4* rrow) {
   using X = Sh<D, C>;
   const int lane = threadIdx.x & 31, quad = lane & 3, row = lane >> 2;
   const int nt = ceil_div(run.n, kTT);
-  const float4* rope4 = reinterpret_cast<const float4*>(a.rope);     // two frequencies: (cos, sin, cos, sin)
-  const uint32_t stage0 = smem_addr(stages), vs0 = smem_addr(bk.Vs);
+  const uint32_t vs0 = smem_addr(bk.Vs);
   const float inv[2] = {qinv[0] * bk.kinv, qinv[1] * bk.kinv};
-  int ids = 0, ids_at = -32;                                         // physical pages [ids_at, ids_at + 32) of the run
-  auto fetch = [&](int t) {                                          // tile t's codes into its stage
-    const int pp = 2 * t;
-    if (pp - ids_at >= 32) {
-      ids_at = pp;
-      ids = phys_page(g, run.lead, min(run.pg0 + pp + lane, run.pg_end - 1));
-      if (ids < 0) {
-        set_status(a.st, LVQ_ECAPACITY);
-        ids = 0;
-      }
-    }
-    const int i0 = __shfl_sync(0xffffffffu, ids, pp - ids_at), i1 = __shfl_sync(0xffffffffu, ids, pp + 1 - ids_at);
-    const uint32_t dst = stage0 + (t % X::NST) * X::STAGE;
-    constexpr int VP = X::PAGE / 16;
+  float2 wc[X::NW], ws[X::NW], ec[X::NW], es[X::NW];
 #pragma unroll
-    for (int v = lane; v < 4 * VP; v += 32) {
-      const int id = (v / VP) & 1 ? i1 : i0;
-      cp_async16(dst + v * 16, (v < 2 * VP ? run.kcode : run.vcode) + (size_t)id * X::PAGE + v % VP * 16);
-    }
-    if (t % 8 == 0 && lane < X::F / 2)                               // the RoPE row of its first page
-      cp_async16(smem_addr(rrow) + lane * 16, rope4 + (size_t)(run.pg0 + pp + (g.S >> 3)) * (X::F / 2) + lane);
-  };
-#pragma unroll
-  for (int t = 0; t < X::NST - 1; ++t) {
-    if (t < nt) fetch(t);
-    cp_commit();
+  for (int w = 0; w < X::NW; ++w) {
+    const float4 x = bk.E8[w * 4 + quad];
+    ec[w] = make_float2(x.x, x.y);
+    es[w] = make_float2(x.z, x.w);
   }
-  float2 wc[X::NW], ws[X::NW];
   for (int t = 0; t < nt; ++t) {
     cp_wait<X::NST - 2>();
     __syncwarp();
@@ -415,8 +440,8 @@ __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, con
             mma_f16(sl[u], qf[0][w], rl, zl);
             if constexpr (!STK) mma_f16(sl[u], qf[STK ? 0 : 1][w], rh, zh);
             mma_f16(sh[u], qf[0][w], rh, zh);
-            wc[w] = make_float2(c.x * bk.ec[w].x - s.x * bk.es[w].x, c.y * bk.ec[w].y - s.y * bk.es[w].y);
-            ws[w] = __ffma2_rn(s, bk.ec[w], __fmul2_rn(c, bk.es[w]));
+            wc[w] = make_float2(c.x * ec[w].x - s.x * es[w].x, c.y * ec[w].y - s.y * es[w].y);
+            ws[w] = __ffma2_rn(s, ec[w], __fmul2_rn(c, es[w]));
           }
         }
       }
@@ -517,7 +542,7 @@ __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, con
       }
     }
     __syncwarp();                                                    // the stage is read
-    if (t + X::NST - 1 < nt) fetch(t + X::NST - 1);
+    if (t + X::NST - 1 < nt) fetch_tile<D, C>(g, a, run, t + X::NST - 1, stages, rrow);
     cp_commit();
   }
   cp_wait<0>();
@@ -526,109 +551,135 @@ __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, con
 
 // The bf16 tokens [i0, i1) of request b's list (sink tokens, then recent ones) against NR query heads, on
 // CUDA cores: D / 4 lanes to a token, a lane two frequencies (channels 2 f, 2 f + 1 and their partners) of
-// the key and four channels of the value; the rotation moves on by a token at a time.  Eight tokens (16 at
-// d = 64) are loaded at once.  Row r's outputs are joined with what its area row holds (`fresh`: nothing yet).
+// the key and four channels of the value; within a batch of 8 tokens (16 at d = 64) the rotation moves on by a
+// token at a time.  A batch and its RoPE row are loaded while the one before is worked on; the first one's loads
+// go out together with the query's, so that an entry waits for memory once.  Row r's outputs are joined with what
+// its area row holds (`fresh`: nothing yet).
 template <int D, int C, int NR>
 __device__ __forceinline__ void bf16_run(const Geo& g, const SharedArgs& a, const Counters& c, int b, int h, const __nv_bfloat16* q,
                                          float scale, int i0, int i1, float* area, float2* ml, bool fresh) {
   using X = Sh<D, C>;
-  constexpr int LPT = D / 4, TPW = 32 / LPT, NB = 8;
+  constexpr int LPT = D / 4, TPW = 32 / LPT, NB = 8, BT = NB * TPW;
   const int lane = threadIdx.x & 31, fp = lane % LPT, half = lane / LPT;
   const float4* rope4 = reinterpret_cast<const float4*>(a.rope);
-  auto angle = [&](int p) {                                          // (cos, cos, sin, sin) at position p
-    const float4 x = __ldg(rope4 + (size_t)(p >> 3) * (X::F / 2) + fp), y = __ldg(rope4 + (size_t)(g.RC + (p & 7)) * (X::F / 2) + fp);
-    return make_float4(x.x * y.x - x.y * y.y, x.z * y.z - x.w * y.w, x.x * y.y + x.y * y.x, x.z * y.w + x.w * y.z);
+  struct Turn { float4 x, y; };                                      // rows of the coarse and fine tables, two frequencies
+  auto turn_at = [&](int p) {
+    Turn t;
+    t.x = __ldg(rope4 + (size_t)(p >> 3) * (X::F / 2) + fp);
+    t.y = __ldg(rope4 + (size_t)(g.RC + (p & 7)) * (X::F / 2) + fp);
+    return t;
+  };
+  auto angle = [](const Turn& t) {                                   // (cos, cos, sin, sin)
+    return make_float4(t.x.x * t.y.x - t.x.y * t.y.y, t.x.z * t.y.z - t.x.w * t.y.w, t.x.x * t.y.y + t.x.y * t.y.x,
+                       t.x.z * t.y.w + t.x.w * t.y.z);
   };
   const int ctx = c.ctx[b], coded = c.coded[b], S_eff = min(g.S, ctx);
-  float4 z[NR];                                                      // rotated queries: channels f, f + 1, f + d/2, f + 1 + d/2
-  const float4 wq = angle(ctx - 1);
+  const int s1 = min(i1, S_eff), r0 = max(i0, S_eff);                // sink tokens [i0, s1), recent ones [r0, i1)
+  const int nsb = max(0, ceil_div(s1 - i0, BT)), n_batch = nsb + max(0, ceil_div(i1 - r0, BT));
+  const __nv_bfloat16* sk = a.sink + sink_off(g, a.layer, 0, a.step, b, h, 0);
+  const __nv_bfloat16* sv = a.sink + sink_off(g, a.layer, 1, a.step, b, h, 0);
+  const __nv_bfloat16* rk = a.ring + ring_off(g, a.layer, 0, a.step, b, h, 0);
+  const __nv_bfloat16* rv = a.ring + ring_off(g, a.layer, 1, a.step, b, h, 0);
+  // batch n: its first token of the list, how many it holds, its keys, values and rotation
+  struct Batch {
+    uint32_t kx[NB], ky[NB];
+    uint2 v[NB];
+    Turn t;
+  };
+  auto load = [&](int n, Batch& x) {
+    const bool sink = n < nsb;
+    const int t0 = sink ? i0 + n * BT : r0 + (n - nsb) * BT, end = sink ? s1 : i1;
+    const __nv_bfloat16 *kb = sink ? sk : rk, *vb = sink ? sv : rv;
+    int slot = sink ? t0 + half : (coded + t0 - S_eff + half) % g.R;
+    // (a lane of a token past the last one may start past it: its position only has to lie within the tables)
+    x.t = turn_at(min((sink ? t0 : g.S + coded + t0 - S_eff) + half, g.max_ctx - 1));
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      x.kx[u] = x.ky[u] = 0u;
+      x.v[u] = make_uint2(0u, 0u);
+      if (t0 + u * TPW + half < end) {
+        const uint32_t* kr = reinterpret_cast<const uint32_t*>(kb + (size_t)slot * D);
+        x.kx[u] = __ldg(kr + fp);
+        x.ky[u] = __ldg(kr + fp + X::F / 2);
+        x.v[u] = __ldg(reinterpret_cast<const uint2*>(vb + (size_t)slot * D) + fp);
+      }
+      slot += TPW;
+      if (!sink && slot >= g.R) slot -= g.R;                          // (TPW <= R)
+    }
+  };
+  Batch cur;
+  load(0, cur);
+  const Turn tq = turn_at(ctx - 1), td = turn_at(TPW);
+  uint32_t qx[NR], qy[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     const uint32_t* qr = reinterpret_cast<const uint32_t*>(q + (size_t)r * D);
-    const float2 x = b2_lohi(__ldg(qr + fp)), y = b2_lohi(__ldg(qr + fp + X::F / 2));
-    z[r] = make_float4((x.x * wq.x - y.x * wq.z) * scale, (x.y * wq.y - y.y * wq.w) * scale, (y.x * wq.x + x.x * wq.z) * scale,
-                       (y.y * wq.y + x.y * wq.w) * scale);
+    qx[r] = __ldg(qr + fp);
+    qy[r] = __ldg(qr + fp + X::F / 2);
   }
-  const float4 dw = angle(TPW);
+  const float4 wq = angle(tq), dw = angle(td);
+  float4 z[NR];                                                      // rotated queries: channels f, f + 1, f + d/2, f + 1 + d/2
   float m[NR], l[NR], o[NR][4];
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
+    const float2 x = b2_lohi(qx[r]), y = b2_lohi(qy[r]);
+    z[r] = make_float4((x.x * wq.x - y.x * wq.z) * scale, (x.y * wq.y - y.y * wq.w) * scale, (y.x * wq.x + x.x * wq.z) * scale,
+                       (y.y * wq.y + x.y * wq.w) * scale);
     m[r] = kNoMax;
     l[r] = o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
   }
 #pragma unroll 1
-  for (int src = 0; src < 2; ++src) {
-    const int ra = src == 0 ? i0 : max(i0, S_eff), rb = src == 0 ? min(i1, S_eff) : i1;
-    if (ra >= rb) continue;
-    const __nv_bfloat16* kb = src == 0 ? a.sink + sink_off(g, a.layer, 0, a.step, b, h, 0) : a.ring + ring_off(g, a.layer, 0, a.step, b, h, 0);
-    const __nv_bfloat16* vb = src == 0 ? a.sink + sink_off(g, a.layer, 1, a.step, b, h, 0) : a.ring + ring_off(g, a.layer, 1, a.step, b, h, 0);
-    const int p0 = src == 0 ? ra : g.S + coded + ra - S_eff;
-    int slot = src == 0 ? ra + half : (coded + ra - S_eff + half) % g.R;
-    // (lanes of a token past the last one may start past it: their position only has to lie within the tables)
-    float4 w = angle(min(p0 + half, g.max_ctx - 1));
-#pragma unroll 1
-    for (int t0 = ra; t0 < rb; t0 += NB * TPW) {
-      uint32_t kx[NB], ky[NB];
-      uint2 vv[NB];
+  for (int n = 0; n < n_batch; ++n) {
+    Batch nxt;
+    if (NR == 1 && n + 1 < n_batch) load(n + 1, nxt);              // (more rows have no registers to spare)
+    const int left = (n < nsb ? s1 - i0 - n * BT : i1 - r0 - (n - nsb) * BT) - half;   // tokens from the lane's first on
+    float4 w = angle(cur.t);
+    float d[NR][NB];
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const float2 x = b2_lohi(cur.kx[u]), y = b2_lohi(cur.ky[u]);
+      const float k0 = x.x * w.x - y.x * w.z, k1 = x.y * w.y - y.y * w.w, k2 = y.x * w.x + x.x * w.z, k3 = y.y * w.y + x.y * w.w;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) d[r][u] = z[r].x * k0 + z[r].y * k1 + (z[r].z * k2 + z[r].w * k3);
+      w = make_float4(w.x * dw.x - w.z * dw.z, w.y * dw.y - w.w * dw.w, w.z * dw.x + w.x * dw.z, w.w * dw.y + w.y * dw.w);
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      // lane sums, transposed: a lane keeps token fp % 8 of its token group
+#pragma unroll
+      for (int hb = NB / 2; hb > 0; hb >>= 1) {
+        const bool up = (fp & hb) != 0;
+#pragma unroll
+        for (int k = 0; k < hb; ++k) {
+          const float send = up ? d[r][k] : d[r][k + hb], keep = up ? d[r][k + hb] : d[r][k];
+          d[r][k] = keep + __shfl_xor_sync(0xffffffffu, send, hb);
+        }
+      }
+      float s = d[r][0];
+#pragma unroll
+      for (int o2 = NB; o2 < LPT; o2 <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o2);
+      if ((fp & (NB - 1)) * TPW >= left) s = -INFINITY;
+      float top = s;
+#pragma unroll
+      for (int o2 = 1; o2 < NB; o2 <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+      if (TPW == 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      const float mn = fmaxf(m[r], top), al = ex2(m[r] - mn), p = ex2(s - mn);
+      m[r] = mn;
+      l[r] = l[r] * al + (fp < NB ? p : 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[r][k] *= al;
 #pragma unroll
       for (int u = 0; u < NB; ++u) {
-        kx[u] = ky[u] = 0u;
-        vv[u] = make_uint2(0u, 0u);
-        if (t0 + u * TPW + half < rb) {
-          const uint32_t* kr = reinterpret_cast<const uint32_t*>(kb + (size_t)slot * D);
-          kx[u] = __ldg(kr + fp);
-          ky[u] = __ldg(kr + fp + X::F / 2);
-          vv[u] = __ldg(reinterpret_cast<const uint2*>(vb + (size_t)slot * D) + fp);
-        }
-        slot += TPW;
-        if (src == 1 && slot >= g.R) slot -= g.R;                     // (TPW <= R)
-      }
-      float d[NR][NB];
-#pragma unroll
-      for (int u = 0; u < NB; ++u) {
-        const float2 x = b2_lohi(kx[u]), y = b2_lohi(ky[u]);
-        const float k0 = x.x * w.x - y.x * w.z, k1 = x.y * w.y - y.y * w.w, k2 = y.x * w.x + x.x * w.z, k3 = y.y * w.y + x.y * w.w;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) d[r][u] = z[r].x * k0 + z[r].y * k1 + (z[r].z * k2 + z[r].w * k3);
-        w = make_float4(w.x * dw.x - w.z * dw.z, w.y * dw.y - w.w * dw.w, w.z * dw.x + w.x * dw.z, w.w * dw.y + w.y * dw.w);
-      }
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        // lane sums, transposed: lane keeps token tk = bits (4 2 1 of fp's low bits) of its token group
-#pragma unroll
-        for (int hb = NB / 2; hb > 0; hb >>= 1) {
-          const bool up = (fp & hb) != 0;
-#pragma unroll
-          for (int k = 0; k < hb; ++k) {
-            const float send = up ? d[r][k] : d[r][k + hb], keep = up ? d[r][k + hb] : d[r][k];
-            d[r][k] = keep + __shfl_xor_sync(0xffffffffu, send, hb);
-          }
-        }
-        float s = d[r][0];
-#pragma unroll
-        for (int o2 = NB; o2 < LPT; o2 <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o2);
-        const int tk = fp & (NB - 1);
-        if (t0 + tk * TPW + half >= rb) s = -INFINITY;
-        float top = s;
-#pragma unroll
-        for (int o2 = 1; o2 < NB; o2 <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
-        if (TPW == 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        const float mn = fmaxf(m[r], top), al = ex2(m[r] - mn), p = ex2(s - mn);
-        m[r] = mn;
-        l[r] = l[r] * al + (fp < NB ? p : 0.f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[r][k] *= al;
-#pragma unroll
-        for (int u = 0; u < NB; ++u) {
-          const float pu = __shfl_sync(0xffffffffu, p, u + half * LPT);
-          const float2 v0 = b2_lohi(vv[u].x), v1 = b2_lohi(vv[u].y);
-          o[r][0] = fmaf(pu, v0.x, o[r][0]);
-          o[r][1] = fmaf(pu, v0.y, o[r][1]);
-          o[r][2] = fmaf(pu, v1.x, o[r][2]);
-          o[r][3] = fmaf(pu, v1.y, o[r][3]);
-        }
+        const float pu = __shfl_sync(0xffffffffu, p, u + half * LPT);
+        const float2 v0 = b2_lohi(cur.v[u].x), v1 = b2_lohi(cur.v[u].y);
+        o[r][0] = fmaf(pu, v0.x, o[r][0]);
+        o[r][1] = fmaf(pu, v0.y, o[r][1]);
+        o[r][2] = fmaf(pu, v1.x, o[r][2]);
+        o[r][3] = fmaf(pu, v1.y, o[r][3]);
       }
     }
+    if (NR == 1) cur = nxt;
+    else if (n + 1 < n_batch) load(n + 1, cur);
   }
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
@@ -699,6 +750,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   unsigned char* area = sm + X::OFF_W + warp * X::WARP;
   float* area_f = reinterpret_cast<float*>(area);
   float4* Ff = reinterpret_cast<float4*>(sm + X::OFF_F);
+  float4* E8 = reinterpret_cast<float4*>(sm + X::OFF_E);
   float4* rrow = reinterpret_cast<float4*>(sm + X::OFF_R) + warp * (X::F / 2);
   float2* ml_s = reinterpret_cast<float2*>(sm + X::OFF_ML);   // [warp][16]: rows of the area (own entries: 8, then 8 parked)
   float2* ml = ml_s + warp * kQT;
@@ -723,32 +775,31 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   }
   dependency_wait();
   dependents_may_launch();
+  Book<D, C> bk;
+  bk.Ks = Ks; bk.Vs = Vs; bk.Ff = Ff; bk.E8 = E8;
+  const float4* rope4 = reinterpret_cast<const float4*>(a.rope);   // two frequencies: (cos, sin, cos, sin)
+  auto pair_of = [&](int w) { return ((quad + 4 * (w / (C / 2))) * C + 2 * (w % (C / 2))) / 2; };   // lane's frequency pair w
+  if (warp < X::NW && row == 0) {
+    const float4 x = __ldcg(rope4 + X::F / 2 + pair_of(warp));
+    E8[warp * 4 + quad] = make_float4(x.x, x.z, x.y, x.w);
+  }
+  // the small loads first: the slices' 2 x 32 or 2 x 64 KB a CTA keep the way from L2 busy for some 2000 cycles
+  const bool ok = load_counters(g, a, c, reinterpret_cast<long long*>(sm + X::OFF_P), j == 0 && h == 0);   // (its barriers publish the mbarrier)
   if (tid == 0) {
     mbar_expect_tx(bar, 2 * X::KS);
     bulk_g2s(smem_addr(Ks), kslice, X::KS, bar);
-    bulk_g2s(smem_addr(sm + X::OFF_W), vslice, X::KS, bar);
+    bulk_g2s(smem_addr(Vs), vslice, X::KS, bar);
   }
-  const bool ok = load_counters(g, a, c, reinterpret_cast<long long*>(sm + X::OFF_P), j == 0 && h == 0);   // (its barriers publish the mbarrier)
   // every slot of this part starts empty
   for (int i = tid; i < a.batch * rep * 2; i += kShThreads) {
     const int b = i / (rep * 2), r = i / 2 % rep;
     a.pml[(((size_t)b * g.Hq + h * rep + r) * g.max_splits + j) * 2 + (i & 1)] = make_float2(kNoMax, 0.f);
   }
-  Book<D, C> bk;
-  bk.Ks = Ks; bk.Vs = Vs; bk.Ff = Ff;
-  const float4* rope4 = reinterpret_cast<const float4*>(a.rope);   // two frequencies: (cos, sin, cos, sin)
-  auto pair_of = [&](int w) { return ((quad + 4 * (w / (C / 2))) * C + 2 * (w % (C / 2))) / 2; };   // lane's frequency pair w
   if (warp < X::NW) {
     const int p = (g.S & 7) + row;
     const float4 x = __ldcg(rope4 + (size_t)(p >> 3) * (X::F / 2) + pair_of(warp));
     const float4 y = __ldcg(rope4 + (size_t)(g.RC + (p & 7)) * (X::F / 2) + pair_of(warp));
     Ff[warp * 32 + lane] = make_float4(x.x * y.x - x.y * y.y, x.z * y.z - x.w * y.w, x.x * y.y + x.y * y.x, x.z * y.w + x.w * y.z);
-  }
-#pragma unroll
-  for (int w = 0; w < X::NW; ++w) {
-    const float4 x = __ldcg(rope4 + X::F / 2 + pair_of(w));
-    bk.ec[w] = make_float2(x.x, x.z);
-    bk.es[w] = make_float2(x.y, x.w);
   }
   const float qk_scale = 1.4426950408889634f / sqrtf((float)D);
   // Fragments of a query tile: D / 4 lanes rotate a row at its own position, scale it to fp16's range and split it.
@@ -776,9 +827,9 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   };
   // this part of the head's list: [cut0, cut1), shared entries first; e, qt: where it begins
   const long long shared_total = ok ? c.gcum[a.ng] : 0, total = ok ? shared_total + c.ocum[a.batch] : 0;
-  const long long cut0 = total * j / a.k, cut1 = total * (j + 1) / a.k;
+  const long long cut0 = div_cost(total * j, a.k), cut1 = div_cost(total * (j + 1), a.k);
   int e = a.ng, qt = 0;
-  Entry en = {0, 0, 0};
+  Entry en = {0, 0, 0, 0, 1};
   RowTile rt;
   rt.rep = rep; rt.h = h;
   auto next_tile = [&](bool first) {                           // moves on to the part's next query tile of shared tokens
@@ -787,7 +838,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
       if (e >= a.ng || c.gcum[e] >= cut1) { e = a.ng; return; }
       en = shared_entry(g, c, e);
       if (en.tiles == 0) continue;
-      for (qt = first ? (cut0 > c.gcum[e] ? (int)((cut0 - c.gcum[e]) / en.each()) : 0) : qt + 1; qt < en.qtiles; ++qt) {
+      for (qt = first ? (cut0 > c.gcum[e] ? (int)div_cost(cut0 - c.gcum[e], en.each()) : 0) : qt + 1; qt < en.qtiles; ++qt) {
         const long long base = c.gcum[e] + qt * en.each() + en.fixed;
         if (base >= cut1) { e = a.ng; return; }
         if (max(0ll, cut0 - base) < min((long long)en.tiles, cut1 - base)) {
@@ -799,9 +850,27 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
       }
     }
   };
+  // the warp's share of the query tile's tokens, its first codes on their way
+  Run run;
+  auto start_shared = [&]() {
+    const long long base = c.gcum[e] + qt * en.each() + en.fixed;
+    const int t0 = (int)max(0ll, cut0 - base), t1 = (int)min((long long)en.tiles, cut1 - base);
+    const int w0 = t0 + (int)((long long)(t1 - t0) * warp / kWarps), w1 = t0 + (int)((long long)(t1 - t0) * (warp + 1) / kWarps);
+    run.lead = c.lead[e];
+    run.pg0 = 2 * w0;
+    run.n = w0 < w1 ? min(w1 * kTT, c.sh[e]) - w0 * kTT : 0;
+    run.pg_end = run.pg0 + ceil_div(run.n, kPage);
+    run.kcode = a.idx + idx_page_off(g, a.layer, blk, run.lead, h, 0, 0);
+    run.vcode = a.idx + idx_page_off(g, a.layer, blk, run.lead, h, 1, 0);
+    run.ids = 0; run.ids_at = -32;
+    begin_run<D, C>(g, a, run, area, rrow);
+  };
   if (ok) {
     next_tile(true);
-    if (e < a.ng) set_queries(rt);
+    if (e < a.ng) {
+      start_shared();
+      set_queries(rt);
+    }
     if (g.pool) check_rows(g, a, c);
   }
   const bool late = __syncthreads_or(!mbar_wait(bar, 0, g.wait_iters));
@@ -810,38 +879,42 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
       set_status(a.st, LVQ_ETIMEOUT);
       mbar_wait(bar, 0, g.wait_iters);                         // the copies land before the CTA exits
     }
+    cp_wait<0>();
     return;
   }
   // the slices' largest finite magnitudes (as bf16 pairs); the values go to their padded rows as scaled fp16
   {
-    const uint4* kw = reinterpret_cast<const uint4*>(Ks);
-    const uint4* vw = reinterpret_cast<const uint4*>(sm + X::OFF_W);
-    auto amax = [](uint4 w, uint32_t m) {
-      m = __vmaxu2(m, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
-      return __vmaxu2(m, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+    constexpr int NV = X::KS / 16 / kShThreads, VPR = D / 8;   // vectors of a thread, of a row
+    // (a NaN never wins a maximum; an infinity, below, counts nothing)
+    auto amax = [](uint4 w, __nv_bfloat162 m) {
+      auto mag = [](uint32_t x) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x)); };
+      return __hmax2(m, __hmax2(__hmax2(mag(w.x), mag(w.y)), __hmax2(mag(w.z), mag(w.w))));
+    };
+    auto widest = [](__nv_bfloat162 m) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+      return max(w & 0xffffu, w >> 16);
     };
     auto finite = [](uint32_t w) {
       w &= 0x7fff7fffu;
-      return ((w & 0xffffu) < 0x7f80u ? w & 0xffffu : 0u) | ((w >> 16) < 0x7f80u ? w & 0xffff0000u : 0u);
+      return max((w & 0xffffu) < 0x7f80u ? w & 0xffffu : 0u, (w >> 16) < 0x7f80u ? w >> 16 : 0u);
     };
-    constexpr int NV = X::KS / 16 / kShThreads;
-    uint32_t ka = 0, va = 0;
+    __nv_bfloat162 k2 = __floats2bfloat162_rn(0.f, 0.f), v2 = k2;
     uint4 v[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      v[i] = vw[tid + i * kShThreads];
-      va = amax(v[i], va);
+      v[i] = reinterpret_cast<const uint4*>(Vs)[tid + i * kShThreads];
+      v2 = amax(v[i], v2);
     }
 #pragma unroll 4
-    for (int i = 0; i < NV; ++i) ka = amax(kw[tid + i * kShThreads], ka);
-    ka = max(ka & 0xffffu, ka >> 16);
-    va = max(va & 0xffffu, va >> 16);
-    if (__any_sync(0xffffffffu, max(ka, va) >= 0x7f80u)) {     // infinities or NaN among the entries: they count nothing
+    for (int i = 0; i < NV; ++i) k2 = amax(reinterpret_cast<const uint4*>(Ks)[tid + i * kShThreads], k2);
+    uint32_t ka = widest(k2), va = widest(v2);
+    if (__any_sync(0xffffffffu, max(ka, va) >= 0x7f80u)) {
       ka = va = 0;
-      for (int i = tid; i < X::KS / 4; i += kShThreads) {
-        const uint32_t k = finite(reinterpret_cast<const uint32_t*>(kw)[i]), v = finite(reinterpret_cast<const uint32_t*>(vw)[i]);
-        ka = max(ka, max(k & 0xffffu, k >> 16));
-        va = max(va, max(v & 0xffffu, v >> 16));
+#pragma unroll 1
+      for (int i = tid; i < X::KS / 16; i += kShThreads) {
+        const uint4 k = reinterpret_cast<const uint4*>(Ks)[i], x = reinterpret_cast<const uint4*>(Vs)[i];
+        ka = max(ka, max(max(finite(k.x), finite(k.y)), max(finite(k.z), finite(k.w))));
+        va = max(va, max(max(finite(x.x), finite(x.y)), max(finite(x.z), finite(x.w))));
       }
     }
     ka = __reduce_max_sync(0xffffffffu, ka);
@@ -853,12 +926,12 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
     bk.ks = pow2i(fit_exp(ka));
     bk.kinv = pow2i(-fit_exp(ka));
     const float vscale = pow2i(fit_exp(va) + 1);
+    // (every vector is in registers: the rows are spread out in place)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int at = tid + i * kShThreads;
       auto cv = [&](uint32_t x) { return pack_h2(bf16_lo(x) * vscale, bf16_hi(x) * vscale); };
-      *reinterpret_cast<uint4*>(Vs + (at / (D / 8)) * X::VROW + (at % (D / 8)) * 16) =
-          make_uint4(cv(v[i].x), cv(v[i].y), cv(v[i].z), cv(v[i].w));
+      *(reinterpret_cast<uint4*>(Vs + (at / VPR) * X::VROW) + at % VPR) = make_uint4(cv(v[i].x), cv(v[i].y), cv(v[i].z), cv(v[i].w));
     }
     if (tid == 0) red[2 * kWarps] = __float_as_uint(pow2i(-fit_exp(va) - 1));
     __syncthreads();
@@ -869,8 +942,6 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   // ---- shared entries: the CTA's warps share out the tiles of one query tile at a time
   while (e < a.ng) {
     {
-      const long long base = c.gcum[e] + qt * en.each() + en.fixed;
-      const int t0 = (int)max(0ll, cut0 - base), t1 = (int)min((long long)en.tiles, cut1 - base);
       uint32_t qf[2][X::NW][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -882,17 +953,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
       const float qinv[2] = {inv_s[row], inv_s[row + 8]};
       State<D, C> st;
       st.clear();
-      const int w0 = t0 + (int)((long long)(t1 - t0) * warp / kWarps), w1 = t0 + (int)((long long)(t1 - t0) * (warp + 1) / kWarps);
-      if (w0 < w1) {
-        Run run;
-        run.lead = c.lead[e];
-        run.pg0 = 2 * w0;
-        run.n = min(w1 * kTT, c.sh[e]) - w0 * kTT;
-        run.pg_end = run.pg0 + ceil_div(run.n, kPage);
-        run.kcode = a.idx + idx_page_off(g, a.layer, blk, run.lead, h, 0, 0);
-        run.vcode = a.idx + idx_page_off(g, a.layer, blk, run.lead, h, 1, 0);
-        coded_run<D, C, false>(g, a, bk, run, st, qf, qinv, area, rrow);
-      }
+      if (run.n > 0) coded_run<D, C, false>(g, a, bk, run, st, qf, qinv, area, rrow);
       // the warps' results are joined
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -933,6 +994,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
       next_tile(false);
       if (e < a.ng) set_queries(rt);                           // (every warp is past reading the last ones)
       __syncthreads();
+      if (e < a.ng) start_shared();                            // (and the areas are read)
     }
   }
 
@@ -949,19 +1011,32 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
       const Entry en = own_entry(g, c, b);
       if (en.tiles == 0) continue;
       const long long eat = c.ocum[b];
-      for (int qt = x0 > eat ? (int)min((long long)en.qtiles, (x0 - eat) / en.each()) : 0; qt < en.qtiles; ++qt) {
+      for (int qt = x0 > eat ? (int)min((long long)en.qtiles, div_cost(x0 - eat, en.each())) : 0; qt < en.qtiles; ++qt) {
         const long long base = eat + qt * en.each() + en.fixed;
         if (base >= x1) break;
-        const int ta = (int)max(0ll, x0 - base), tb = (int)min((long long)en.tiles, x1 - base);
+        auto tile = [&](long long x) { return en.tile_at((int)min((long long)en.units(), max(0ll, x - base))); };
+        const int ta = tile(x0), tb = tile(x1);
         if (ta >= tb) continue;
-        const int Ta = (int)max(0ll, o0 - base), Tb = (int)min((long long)en.tiles, o1 - base);   // the part's share
+        const int Ta = tile(o0), Tb = tile(o1);                // the part's share
         any = 1;
         const int nrows = min(kOT, rep - qt * kOT);
         const __nv_bfloat16* q = a.q + ((size_t)b * g.Hq + h * rep + qt * kOT) * D;
         const int own0 = c.own0[b], rest = c.coded[b] - own0, nc = ceil_div(rest, kTT);
         const bool coded = ta < nc;
         if (coded) {
-          uint4* Qf = reinterpret_cast<uint4*>(area);          // [k step][lane]: high parts in registers 0, 2, low in 1, 3
+          run.lead = b;
+          run.pg0 = own0 / kPage + 2 * ta;
+          run.n = min(min(tb, nc) * kTT, rest) - ta * kTT;
+          run.pg_end = run.pg0 + ceil_div(run.n, kPage);
+          run.kcode = a.idx + idx_page_off(g, a.layer, blk, b, h, 0, 0);
+          run.vcode = a.idx + idx_page_off(g, a.layer, blk, b, h, 1, 0);
+          run.ids = 0; run.ids_at = -32;
+          // fragments [k step][lane], high parts in registers 0, 2, low in 1, 3: of up to two rows in a place of their own,
+          // so that the codes can be on their way meanwhile; of more in the stages
+          const bool small = nrows <= 2;
+          uint4* Qf = small ? reinterpret_cast<uint4*>(sm + X::OFF_Q) + warp * (X::NW * 8) : reinterpret_cast<uint4*>(area);
+          const int ql = small ? 8 : 32;
+          if (small) begin_run<D, C>(g, a, run, area, rrow);
           constexpr int LPR = D / 4, RPW = 32 / LPR;
           const int f2 = lane % LPR, P = 2 * f2 / C, sub = 2 * f2 % C / 2;
           for (int r0 = 0; r0 < nrows; r0 += RPW) {
@@ -973,7 +1048,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
             split_h2(x, f.x, f.y);
             split_h2(y, f.z, f.w);
             if (r < nrows) {
-              Qf[(P / 4 * (C / 2) + sub) * 32 + r * 4 + P % 4] = f;
+              Qf[(P / 4 * (C / 2) + sub) * ql + r * 4 + P % 4] = f;
               if (f2 == 0) ml[r].x = inv;
             }
           }
@@ -981,7 +1056,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
           uint32_t qf[1][X::NW][4];
 #pragma unroll
           for (int w = 0; w < X::NW; ++w) {
-            const uint4 u = row < nrows ? Qf[w * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 u = row < nrows ? Qf[w * ql + lane] : make_uint4(0u, 0u, 0u, 0u);
             qf[0][w][0] = u.x; qf[0][w][1] = u.y; qf[0][w][2] = u.z; qf[0][w][3] = u.w;
           }
           const float qi = row < nrows ? ml[row].x : 1.f;
@@ -989,13 +1064,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
           __syncwarp();
           State<D, C> st;
           st.clear();
-          Run run;
-          run.lead = b;
-          run.pg0 = own0 / kPage + 2 * ta;
-          run.n = min(min(tb, nc) * kTT, rest) - ta * kTT;
-          run.pg_end = run.pg0 + ceil_div(run.n, kPage);
-          run.kcode = a.idx + idx_page_off(g, a.layer, blk, b, h, 0, 0);
-          run.vcode = a.idx + idx_page_off(g, a.layer, blk, b, h, 1, 0);
+          if (!small) begin_run<D, C>(g, a, run, area, rrow);
           coded_run<D, C, true>(g, a, bk, run, st, qf, qinv, area, rrow);
           st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], 1);
           st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], 2);
