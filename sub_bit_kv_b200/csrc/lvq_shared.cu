@@ -27,7 +27,7 @@ namespace {
 constexpr int kQT = 16;                 // query rows of a tile of shared tokens
 constexpr int kOT = 8;                  // query heads of a tile of own tokens
 constexpr int kTT = 16;                 // tokens of a tile: two pages
-constexpr int kSharedCost = 20;         // fixed cost of a query tile of a shared entry, in token tiles
+constexpr int kSharedCost = 8;          // fixed cost of a query tile of a shared entry, in token tiles
 constexpr int kOwnCost = 4;             // the same of an own entry
 constexpr int kWarps = 8;
 constexpr int kShThreads = 32 * kWarps;
@@ -372,22 +372,20 @@ __device__ inline void add_values(float (&o)[4], const uint32_t (&ph)[4], const 
 // page (8 positions) with one complex multiplication and is taken anew from the tables every 16 pages.  Keys
 // and queries enter as sums of two fp16 values, good to 2^-22 of the largest; lo x lo is left out of 16 rows.
 // Weights too are sums of two fp16 values; values are exact.
+// Query fragments: qf in registers (stacked rows), or qs in shared memory, [hi, lo][k step] 32 lanes apart.
 template <int D, int C, bool STK>
 __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, const Book<D, C>& bk, Run& run, State<D, C>& st,
-                                          const uint32_t (&qf)[STK ? 1 : 2][Sh<D, C>::NW][4], const float (&qinv)[2],
+                                          const uint32_t (&qf)[Sh<D, C>::NW][4], const uint4* qs, const float (&qinv)[2],
                                           unsigned char* stages, float4* rrow) {
   using X = Sh<D, C>;
   const int lane = threadIdx.x & 31, quad = lane & 3, row = lane >> 2;
   const int nt = ceil_div(run.n, kTT);
   const uint32_t vs0 = smem_addr(bk.Vs);
   const float inv[2] = {qinv[0] * bk.kinv, qinv[1] * bk.kinv};
-  float2 wc[X::NW], ws[X::NW], ec[X::NW], es[X::NW];
-#pragma unroll
-  for (int w = 0; w < X::NW; ++w) {
-    const float4 x = bk.E8[w * 4 + quad];
-    ec[w] = make_float2(x.x, x.y);
-    es[w] = make_float2(x.z, x.w);
-  }
+  // (queries and e^{i 8 theta} come from shared memory at every use: held in registers, they left the tile's loads and
+  // products too few to overlap -- 161 us against 178 for 32 requests behind 32K tokens)
+  const float4* e8 = bk.E8 + quad;
+  float2 wc[X::NW], ws[X::NW];
   for (int t = 0; t < nt; ++t) {
     cp_wait<X::NST - 2>();
     __syncwarp();
@@ -428,20 +426,33 @@ __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, con
 #pragma unroll
         for (int v = 0; v < (C < 8 ? C / 2 : 4); ++v) {
           const int w = i * (C / 2) + q * 4 + v;
+          uint32_t qh[4];
+          if constexpr (STK) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) qh[k] = qf[w][k];
+          } else {
+            const uint4 x = qs[w * 32];
+            qh[0] = x.x; qh[1] = x.y; qh[2] = x.z; qh[3] = x.w;
+          }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float2 x = b2_lohi(lo[u][v]), y = b2_lohi(hi[u][v]), c = wc[w], s = ws[w];
+            const float2 kx = b2_lohi(lo[u][v]), ky = b2_lohi(hi[u][v]), c = wc[w], s = ws[w];
             // (scalar where a sign changes: packed operands have none to spare)
-            const float2 r = make_float2(x.x * c.x - y.x * s.x, x.y * c.y - y.y * s.y);
-            const float2 z = __ffma2_rn(y, c, __fmul2_rn(x, s));
+            const float2 r = make_float2(kx.x * c.x - ky.x * s.x, kx.y * c.y - ky.y * s.y);
+            const float2 z = __ffma2_rn(ky, c, __fmul2_rn(kx, s));
             uint32_t rh, rl, zh, zl;
             split_h2(r, rh, rl);
             split_h2(z, zh, zl);
-            mma_f16(sl[u], qf[0][w], rl, zl);
-            if constexpr (!STK) mma_f16(sl[u], qf[STK ? 0 : 1][w], rh, zh);
-            mma_f16(sh[u], qf[0][w], rh, zh);
-            wc[w] = make_float2(c.x * ec[w].x - s.x * es[w].x, c.y * ec[w].y - s.y * es[w].y);
-            ws[w] = __ffma2_rn(s, ec[w], __fmul2_rn(c, es[w]));
+            mma_f16(sl[u], qh, rl, zl);
+            if constexpr (!STK) {
+              const uint4 x = qs[(X::NW + w) * 32];
+              const uint32_t ql[4] = {x.x, x.y, x.z, x.w};
+              mma_f16(sl[u], ql, rh, zh);
+            }
+            mma_f16(sh[u], qh, rh, zh);
+            const float4 e = e8[w * 4];
+            wc[w] = make_float2(c.x * e.x - s.x * e.z, c.y * e.y - s.y * e.w);
+            ws[w] = __ffma2_rn(s, make_float2(e.x, e.y), __fmul2_rn(c, make_float2(e.z, e.w)));
           }
         }
       }
@@ -942,18 +953,11 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   // ---- shared entries: the CTA's warps share out the tiles of one query tile at a time
   while (e < a.ng) {
     {
-      uint32_t qf[2][X::NW][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int w = 0; w < X::NW; ++w) {
-          const uint4 u = reinterpret_cast<const uint4*>(sm + X::OFF_Q)[(i * X::NW + w) * 32 + lane];
-          qf[i][w][0] = u.x; qf[i][w][1] = u.y; qf[i][w][2] = u.z; qf[i][w][3] = u.w;
-        }
       const float qinv[2] = {inv_s[row], inv_s[row + 8]};
       State<D, C> st;
       st.clear();
-      if (run.n > 0) coded_run<D, C, false>(g, a, bk, run, st, qf, qinv, area, rrow);
+      const uint32_t none[X::NW][4] = {};
+      if (run.n > 0) coded_run<D, C, false>(g, a, bk, run, st, none, reinterpret_cast<const uint4*>(sm + X::OFF_Q) + lane, qinv, area, rrow);
       // the warps' results are joined
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -1053,11 +1057,11 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
             }
           }
           __syncwarp();
-          uint32_t qf[1][X::NW][4];
+          uint32_t qf[X::NW][4];
 #pragma unroll
           for (int w = 0; w < X::NW; ++w) {
             const uint4 u = row < nrows ? Qf[w * ql + lane] : make_uint4(0u, 0u, 0u, 0u);
-            qf[0][w][0] = u.x; qf[0][w][1] = u.y; qf[0][w][2] = u.z; qf[0][w][3] = u.w;
+            qf[w][0] = u.x; qf[w][1] = u.y; qf[w][2] = u.z; qf[w][3] = u.w;
           }
           const float qi = row < nrows ? ml[row].x : 1.f;
           const float qinv[2] = {qi, qi};
@@ -1065,7 +1069,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
           State<D, C> st;
           st.clear();
           if (!small) begin_run<D, C>(g, a, run, area, rrow);
-          coded_run<D, C, true>(g, a, bk, run, st, qf, qinv, area, rrow);
+          coded_run<D, C, true>(g, a, bk, run, st, qf, nullptr, qinv, area, rrow);
           st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], 1);
           st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], 2);
           if (row < nrows) {
