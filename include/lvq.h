@@ -343,7 +343,7 @@ LVQ_API int32_t lvq_pool_available(const lvq_pool* pool);
  *   moves: room for n_order + n_order / 2 pairs (source, destination), in the order and form
  *     lvq_compact_pages carries them out; *n_moves receives their number.
  * LVQ_EINVAL for a null pointer, a negative count or an id out of range (outputs then undefined);
- * LVQ_ECAPACITY if host memory is short. */
+ * LVQ_EUNSUPPORTED for n_order above 2^29; LVQ_ECAPACITY if host memory is short. */
 LVQ_API lvq_status lvq_plan_compaction(int32_t n_pages, const int32_t* order, int32_t n_order,
                                        int32_t* new_id, int32_t* moves, int32_t* n_moves);
 
@@ -411,8 +411,10 @@ LVQ_API lvq_status lvq_fork_requests(const lvq_config* cfg, const lvq_layout* la
  *   workspace: as for lvq_decode_attention, whose calls may share it (its counters stay zero).
  * Other arguments as for lvq_decode_attention.  batch <= 256, else LVQ_EUNSUPPORTED.  Sums are
  * taken in a fixed order: the same call gives the same bits.  A request whose counters are
- * outside the layout, or page-table entries out of range: LVQ_ECAPACITY, as there; a group_begin
- * that is not as described: LVQ_EINVAL (outputs then not meaningful). */
+ * outside the layout (its rows come out as 0, lse -inf), or page-table entries out of range:
+ * LVQ_ECAPACITY, as there; a group_begin that is not as described: LVQ_EINVAL (outputs then not
+ * meaningful).  Entries and tokens are scaled by powers of two to the head's largest finite entry,
+ * beside which smaller ones keep 2^-39 of it (keys) and 2^-28 (values) as absolute precision. */
 LVQ_API lvq_status lvq_decode_attention_shared(const lvq_config* cfg, const lvq_layout* lay, int32_t layer,
                                                int32_t step, int32_t batch, const void* q,
                                                const int32_t* ctx_len, const int32_t* coded_len,

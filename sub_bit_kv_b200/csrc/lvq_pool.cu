@@ -129,6 +129,7 @@ lvq_status lvq_pool_renumber(lvq_pool* pool, const int32_t* new_id) try {
 lvq_status lvq_plan_compaction(int32_t n_pages, const int32_t* order, int32_t n_order, int32_t* new_id,
                                int32_t* moves, int32_t* n_moves) try {
   if (n_pages < 1 || n_order < 0 || !new_id || !n_moves || (n_order > 0 && (!order || !moves))) return LVQ_EINVAL;
+  if (n_order > (1 << 29)) return LVQ_EUNSUPPORTED;   // (its moves are counted in 32 bits)
   for (int32_t i = 0; i < n_pages; ++i) new_id[i] = -1;
   std::vector<int32_t> from;
   from.reserve(n_order < n_pages ? n_order : n_pages);

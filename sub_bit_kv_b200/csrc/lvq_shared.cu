@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   if (late || !ok) {
     if (late && tid == 0) {
       set_status(a.st, LVQ_ETIMEOUT);
-      mbar_wait(bar, 0, g.wait_iters);                         // the copies land before the CTA exits
+      mbar_wait(bar, 0, kWaitIters);                           // the copies land before the CTA exits
     }
     cp_wait<0>();
     return;

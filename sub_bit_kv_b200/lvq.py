@@ -302,12 +302,12 @@ def lvq_decode_attention_noalloc(cfg, lay, layer, step, batch, q, ctx_len, coded
         _ptr(dev_status, "dev_status", torch.int32, 4), _stream(stream)), "lvq_decode_attention_noalloc")
 
 
-def _on(dev: int, t: Optional[torch.Tensor], name: str, dtype, min_bytes: int, optional=False):
+def _on(dev: int, t: Optional[torch.Tensor], name: str, dtype, min_bytes: int):
     """_ptr for the calls below, which also refuse a tensor of another device than `dev`, the current one."""
-    p = _ptr(t, name, dtype, min_bytes, optional)
-    if p is not None and t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    return p
+    if t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.nbytes >= min_bytes:
+        return t.data_ptr()
+    _ptr(t, name, dtype, min_bytes)             # says what is wrong, unless it is the device
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
 
 
 def _table(cfg, lay, dev: int, page_table):

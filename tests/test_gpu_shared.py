@@ -220,3 +220,90 @@ def test_refusals():
         Sh.run_shared(case, begin, tokens, 0, q.float())
     with pytest.raises(ValueError):
         Sh.run_shared(case, begin, tokens, 0, q[:1])
+
+
+def test_empty_groups_and_one_slot():
+    """Groups without requests, and a layout whose rows have room for a single part."""
+    w = _w("ouro14_g32_b32", n_kv_heads=3, n_q_heads=3)
+    case, begin, tokens = Sh.shared_case(w, [(300, [3, 20]), (64, [9, 0])], recent=[5, 9, 130, 1], max_splits=1)
+    q = synth.queries(w, 0, 1, batch=4).cuda()
+    out, lse = Sh.run_shared(case, [0, 0, 2, 4], [77] + tokens, 1, q)
+    Sh.check_against_oracle(case, 1, q, out, lse)
+    out, lse = Sh.run_shared(case, [0, 2, 2, 4], [tokens[0], 1 << 20, tokens[1]], 1, q)
+    Sh.check_against_oracle(case, 1, q, out, lse)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("name", ["tiny", "ouro14_g16_32k", "ouro14_g32_b32", "ouro14_tc1_32k"])
+def test_nothing_is_read_from_masked_places(name, bad):
+    """Entry 255 of every codebook, the window's slots without a token and the sink's tokens past a short
+    context hold NaN or infinities; no token uses that entry, but the rest of the partial last pages does."""
+    w = _w(name, n_kv_heads=2, n_q_heads=2)
+    case, begin, tokens = Sh.shared_case(w, [(203, [0, 13]), (40, [2]), (0, [0])], recent=[5, 1, 11, 0], ctx=[None, None, None, 2])
+    c = case.cache
+    for (layer, b), (ck, cv) in case.codes.items():
+        for kv, codes in ((0, ck), (1, cv)):
+            codes.clamp_(max=254)
+            room = c.lay.max_pages * 8
+            full = torch.full((codes.shape[0], room, codes.shape[2], codes.shape[3]), 255, dtype=torch.uint8)
+            full[:, :codes.shape[1]] = codes
+            Hl.put_codes(c, layer, b, kv, full.cuda())
+    c.cb_view()[..., 255, :] = bad
+    lvq.lvq_pack_codebooks(case.cfg, c.lay, c.cb, c.cbp, c.cb_norm)
+    ring = c.ring_view()
+    for b in range(4):
+        n_rec = case.ctx[b] - min(w.n_sink, case.ctx[b]) - case.coded[b]
+        dead = [s for s in range(c.lay.ring_tokens) if s not in {(case.coded[b] + i) % c.lay.ring_tokens for i in range(n_rec)}]
+        ring[:, :, :, b, :, dead] = bad
+    c.sink_view()[:, :, :, 3, :, 2:] = bad
+    q = synth.queries(w, 0, 1, batch=4).cuda()
+    for ns in (0, 1):
+        out, lse = Sh.run_shared(case, begin, tokens, 1, q, num_splits=ns)
+        Sh.check_against_oracle(case, 1, q, out, lse)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** 20])
+def test_scale_of_the_entries(scale):
+    """Keys and values far from 1: the operands' powers of two follow the head's largest entry (queries make up for
+    the keys' scale, so that the softmax stays one)."""
+    w = _w("ouro14_g32_b32", n_kv_heads=2, n_q_heads=2)
+    case, begin, tokens = Sh.shared_case(w, [(300, [3, 20])], recent=[70, 9])
+    c = case.cache
+    for t in (c.cb, c.sink, c.ring):
+        t.mul_(scale)
+    case.cb[0].mul_(scale)
+    for d in (case.sink_kv, case.ring_kv):
+        for v in d.values():
+            v.mul_(scale)
+    lvq.lvq_pack_codebooks(case.cfg, c.lay, c.cb, c.cbp, c.cb_norm)
+    q = (synth.queries(w, 0, 1, batch=2) / scale).to(torch.bfloat16).cuda()
+    out, lse = Sh.run_shared(case, begin, tokens, 1, q)
+    Sh.check_against_oracle(case, 1, q, out, lse)
+
+
+def test_zero_codebooks():
+    """All entries zero: the bf16 tokens alone carry values."""
+    w = _w("ouro14_g16_32k", n_kv_heads=1, n_q_heads=2)
+    case, begin, tokens = Sh.shared_case(w, [(96, [3, 20])], recent=[70, 9])
+    case.cache.cbp.zero_()
+    case.cb[0].zero_()
+    q = synth.queries(w, 0, 1, batch=2).cuda()
+    out, lse = Sh.run_shared(case, begin, tokens, 1, q)
+    Sh.check_against_oracle(case, 1, q, out, lse)
+
+
+def test_waits_are_bounded():
+    """With waits cut to a single poll the call ends, with LVQ_ETIMEOUT where the entries were not there yet, and the next one
+    is right."""
+    w = _w("ouro14_g32_b32", n_kv_heads=2, n_q_heads=2)
+    case, begin, tokens = Sh.shared_case(w, [(300, [3, 20])], recent=[70, 9])
+    q = synth.queries(w, 0, 1, batch=2).cuda()
+    lvq.lvq_debug_faults(1, 0)
+    try:
+        Sh.run_shared(case, begin, tokens, 1, q, check=False)
+    finally:
+        lvq.lvq_debug_faults(0, 0)
+    assert int(case.cache.status.item()) in (lvq.LVQ_OK, lvq.LVQ_ETIMEOUT)
+    case.cache.status.zero_()
+    out, lse = Sh.run_shared(case, begin, tokens, 1, q)
+    Sh.check_against_oracle(case, 1, q, out, lse)
