@@ -1242,8 +1242,11 @@ cudaError_t launch_decode_shared(const Geo& g, int layer, int step, int batch, c
   SharedArgs a = {layer, step, batch, n_groups, num_splits, q, ctx_len, coded_len, group_begin, group_tokens,
                   sink, ring, idx, cbp, rope, ws, nullptr, st};
   if (a.k == 0) {
-    // one wave of CTAs, but no part below about 128 of the tokens the layout can hold
-    const long long most = ((long long)batch * g.max_ctx + 127) / 128;
+    // one wave of CTAs; where the layout holds few tokens, two parts a request and two for the shared ones, or one to
+    // 128 tokens (two requests of 464 tokens, one head: 12.3 us with 9 parts, 15.5 with 64, 19.0 with one; four of 20
+    // tokens, 16 heads: 13.9 with 9, 18.2 with one)
+    const long long by_tokens = ((long long)batch * g.max_ctx + 127) / 128, by_batch = 2ll * batch + 2;
+    const long long most = by_tokens > by_batch ? by_tokens : by_batch;
     a.k = n_sm / g.H < 1 ? 1 : n_sm / g.H;
     if (a.k > g.max_splits) a.k = g.max_splits;
     if (a.k > most) a.k = (int)most;
