@@ -27,8 +27,10 @@ namespace {
 constexpr int kQT = 16;                 // query rows of a tile of shared tokens
 constexpr int kOT = 8;                  // query heads of a tile of own tokens
 constexpr int kTT = 16;                 // tokens of a tile: two pages
-constexpr int kSharedCost = 8;          // fixed cost of a query tile of a shared entry, in token tiles
-constexpr int kOwnCost = 4;             // the same of an own entry
+// Costs in token tiles, swept together over 22 shapes (the listed values are their common optimum; a factor of two
+// in any of them costs the geometric mean 1 to 4 %): a query tile of a shared entry as such (fragments, joining the
+// warps), one of an own entry, and what the first part with own entries spends on getting to them.
+constexpr int kSharedCost = 8, kOwnCost = 4, kOwnStage = 20;
 constexpr int kWarps = 8;
 constexpr int kShThreads = 32 * kWarps;
 constexpr float kNoMax = -1e30f;        // softmax reference before the first token
@@ -837,7 +839,8 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
     }
   };
   // this part of the head's list: [cut0, cut1), shared entries first; e, qt: where it begins
-  const long long shared_total = ok ? c.gcum[a.ng] : 0, total = ok ? shared_total + c.ocum[a.batch] : 0;
+  const long long shared_total = ok ? c.gcum[a.ng] : 0, own_total = ok ? c.ocum[a.batch] : 0;
+  const long long own_at = shared_total + (shared_total > 0 && own_total > 0 ? kOwnStage : 0), total = own_at + own_total;
   const long long cut0 = div_cost(total * j, a.k), cut1 = div_cost(total * (j + 1), a.k);
   int e = a.ng, qt = 0;
   Entry en = {0, 0, 0, 0, 1};
@@ -1003,7 +1006,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   }
 
   // ---- own entries: a contiguous run of the part's tiles to a warp
-  const long long o0 = max(0ll, cut0 - shared_total), o1 = max(0ll, cut1 - shared_total);
+  const long long o0 = max(0ll, cut0 - own_at), o1 = max(0ll, cut1 - own_at);
   if (o0 >= o1) return;
   const long long x0 = o0 + (o1 - o0) * warp / kWarps, x1 = o0 + (o1 - o0) * (warp + 1) / kWarps;
   int* park_s = reinterpret_cast<int*>(red) + 2 * kWarps;      // [warp]: entry tile whose beginning another warp has, or -1
