@@ -27,9 +27,9 @@ namespace {
 constexpr int kQT = 16;                 // query rows of a tile of shared tokens
 constexpr int kOT = 8;                  // query heads of a tile of own tokens
 constexpr int kTT = 16;                 // tokens of a tile: two pages
-// Costs in token tiles, swept together over 22 shapes (the listed values are their common optimum; a factor of two
-// in any of them costs the geometric mean 1 to 4 %): a query tile of a shared entry as such (fragments, joining the
-// warps), one of an own entry, and what the first part with own entries spends on getting to them.
+// Costs in token tiles: a query tile of a shared entry as such (fragments, joining the warps), one of an own entry, and
+// what the first part with own entries spends on getting to them.  Swept one after the other over 22 shapes to their
+// least geometric mean, 32.0 us (33.2 without the last one).
 constexpr int kSharedCost = 8, kOwnCost = 4, kOwnStage = 20;
 constexpr int kWarps = 8;
 constexpr int kShThreads = 32 * kWarps;
@@ -751,6 +751,17 @@ __device__ __forceinline__ void query_pair(const Geo& g, const SharedArgs& a, co
 // One CTA per part and KV head, 8 warps.  The step slices of the head are staged once in shared memory, the
 // values as fp16 (scaled by a power of two, so that every bf16 value within 2^-28 of the largest is exact) in
 // rows padded by 16 bytes (8 tokens' entries of one group then fall on different banks as often as not).
+//
+// What bounds it.  The bytes are few (32 requests behind 32K tokens at c = 8: 60.6 MB, 9.2 us); restoring, rotating and
+// splitting a key is some 30 warp instructions a token and 16 rows, products 5 (10.6 cycles of the SM's mma.sync
+// pipe), the rest weights, values and loads: 57 in all.  At 255 registers two warps share a scheduler, which issues
+// 0.36 a cycle (counters: fixed latencies 0.95, pipe throttle 0.72, instruction fetch 0.56, shared memory 0.53 cycles
+// of stall an instruction): 28 cycles a token and 16 rows, 161 us for those 32 requests on an idle stream.
+// Tried and slower: 12 warps of 168 registers (spills: 214 us), values of one tile beside the scores of the next (167
+// to 178), two row tiles to one restored key (156 to 173, and 99 against 86 for 64K with four heads a KV head), and
+// tcgen05 products of 32 rows fed by restoring warps through swizzled shared memory (219 us: M = 128 tiles of 64
+// tokens in two parts; the restoring, softmax and output warps' own instructions, 84 a token, and their hand-offs took
+// 4900 cycles a tile, the tensor core 8 % of them).
 template <int D, int C>
 __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs a) {
   using X = Sh<D, C>;
