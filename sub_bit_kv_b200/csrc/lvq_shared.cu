@@ -91,20 +91,24 @@ __device__ inline int locate(const long long* cum, int n, long long x) {
   return lo;
 }
 
-// cum[i + 1] = the sum of the threads' costs 0 .. i (thread i < n: entry i).  `part`: a value per warp.
-__device__ inline void scan_costs(long long mine, int n, long long* cum, long long* part) {
+// cum[i + 1] = the sum of the threads' costs 0 .. i, of both lists (thread i: entry i of each).  `part`: two values a
+// warp.
+__device__ inline void scan_costs(long long (&up)[2], const Counters& c, int ng, int batch, long long* part) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long up = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, up, o);
-    if (lane >= o) up += v;
-  }
-  if (lane == 31) part[warp] = up;
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const long long v = __shfl_up_sync(0xffffffffu, up[k], o);
+      if (lane >= o) up[k] += v;
+    }
+  if (lane == 31) { part[2 * warp] = up[0]; part[2 * warp + 1] = up[1]; }
   __syncthreads();
-  for (int w = 0; w < warp; ++w) up += part[w];
-  if (tid < n) cum[tid + 1] = up;
-  if (tid == 0) cum[0] = 0;
+  for (int w = 0; w < warp; ++w) { up[0] += part[2 * w]; up[1] += part[2 * w + 1]; }
+  if (tid < ng) c.gcum[tid + 1] = up[0];
+  if (tid < batch) c.ocum[tid + 1] = up[1];
+  if (tid == 0) c.gcum[0] = c.ocum[0] = 0;
+  __syncthreads();
 }
 
 // Loads and checks the counters and derives the costs, a thread to a request and to a group; returns false (for
@@ -153,10 +157,8 @@ __device__ bool load_counters(const Geo& g, const SharedArgs& a, Counters& c, lo
   __syncthreads();
   if (t < a.ng && c.lead[t] == a.batch) c.sh[t] = 0;   // no usable request
   if (t < a.batch) c.own0[t] = ctx > 0 ? c.sh[grp] : 0;
-  scan_costs(t < a.ng ? shared_entry(g, c, t).cost() : 0, a.ng, c.gcum, part);
-  __syncthreads();
-  scan_costs(t < a.batch ? own_entry(g, c, t).cost() : 0, a.batch, c.ocum, part);
-  __syncthreads();
+  long long cost[2] = {t < a.ng ? shared_entry(g, c, t).cost() : 0, t < a.batch ? own_entry(g, c, t).cost() : 0};
+  scan_costs(cost, c, a.ng, a.batch, part);
   return true;
 }
 
@@ -215,7 +217,7 @@ struct Sh {
   static constexpr int OFF_RED = OFF_INV + kQT * 4;
   static constexpr int OFF_BAR = OFF_RED + 4 * kWarps * 4;
   static constexpr int OFF_P = OFF_BAR + 16;
-  static constexpr int OFF_C = OFF_P + kWarps * 8;
+  static constexpr int OFF_C = OFF_P + 2 * kWarps * 8;
   static constexpr int smem(int batch, int ng) { return OFF_C + counter_bytes(batch, ng); }
   static_assert(NP % 4 == 0 && NI * C == 2 * NW, "lane mapping");
   static_assert(NST >= 3 && NST <= 8, "stages (a tile's RoPE row is read before the one 8 tiles on is fetched)");
@@ -803,10 +805,6 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   bk.Ks = Ks; bk.Vs = Vs; bk.Ff = Ff; bk.E8 = E8;
   const float4* rope4 = reinterpret_cast<const float4*>(a.rope);   // two frequencies: (cos, sin, cos, sin)
   auto pair_of = [&](int w) { return ((quad + 4 * (w / (C / 2))) * C + 2 * (w % (C / 2))) / 2; };   // lane's frequency pair w
-  if (warp < X::NW && row == 0) {
-    const float4 x = __ldcg(rope4 + X::F / 2 + pair_of(warp));
-    E8[warp * 4 + quad] = make_float4(x.x, x.z, x.y, x.w);
-  }
   // the small loads first: the slices' 2 x 32 or 2 x 64 KB a CTA keep the way from L2 busy for some 2000 cycles
   const bool ok = load_counters(g, a, c, reinterpret_cast<long long*>(sm + X::OFF_P), j == 0 && h == 0);   // (its barriers publish the mbarrier)
   if (tid == 0) {
@@ -820,9 +818,11 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
     a.pml[(((size_t)b * g.Hq + h * rep + r) * g.max_splits + j) * 2 + (i & 1)] = make_float2(kNoMax, 0.f);
   }
   if (warp < X::NW) {
+    const float4 e = __ldcg(rope4 + X::F / 2 + pair_of(warp));
     const int p = (g.S & 7) + row;
     const float4 x = __ldcg(rope4 + (size_t)(p >> 3) * (X::F / 2) + pair_of(warp));
     const float4 y = __ldcg(rope4 + (size_t)(g.RC + (p & 7)) * (X::F / 2) + pair_of(warp));
+    if (row == 0) E8[warp * 4 + quad] = make_float4(e.x, e.z, e.y, e.w);
     Ff[warp * 32 + lane] = make_float4(x.x * y.x - x.y * y.y, x.z * y.z - x.w * y.w, x.x * y.y + x.y * y.x, x.z * y.w + x.w * y.z);
   }
   const float qk_scale = 1.4426950408889634f / sqrtf((float)D);
@@ -1177,19 +1177,25 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(Geo g, int rows, int 
   dependents_may_launch();
   if (r >= rows) return;
   const size_t slot0 = (size_t)r * g.max_splits * 2;
+  constexpr int NS = 4;                                        // slots of a lane kept in registers: 128 in all
+  float2 x[NS];
   float M = kNoMax;
-  for (int i = lane; i < 2 * k; i += 32) {
-    const float2 x = __ldcg(pml + slot0 + i);
-    if (x.y != 0.f) M = fmaxf(M, x.x);
+#pragma unroll
+  for (int u = 0; u < NS; ++u) x[u] = 32 * u + lane < 2 * k ? __ldcg(pml + slot0 + 32 * u + lane) : make_float2(kNoMax, 0.f);
+#pragma unroll
+  for (int u = 0; u < NS; ++u)
+    if (x[u].y != 0.f) M = fmaxf(M, x[u].x);
+  for (int i = 32 * NS + lane; i < 2 * k; i += 32) {
+    const float2 y = __ldcg(pml + slot0 + i);
+    if (y.y != 0.f) M = fmaxf(M, y.x);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float den = 0.f, acc[V] = {};
-  for (int i0 = 0; i0 < 2 * k; i0 += 32) {
-    const float2 x = i0 + lane < 2 * k ? __ldcg(pml + slot0 + i0 + lane) : make_float2(kNoMax, 0.f);
-    const float w = x.y != 0.f ? ex2(x.x - M) : 0.f;
-    den += w * x.y;
-    unsigned todo = __ballot_sync(0xffffffffu, x.y != 0.f);
+  auto add = [&](float2 y, int i0) {                           // slots i0 .. i0 + 31, one a lane
+    const float w = y.y != 0.f ? ex2(y.x - M) : 0.f;
+    den += w * y.y;
+    unsigned todo = __ballot_sync(0xffffffffu, y.y != 0.f);
     while (todo) {                                             // four partials at a time, in slot order
       float f[4];
       float v[4][V];
@@ -1207,7 +1213,11 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(Geo g, int rows, int 
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] = fmaf(f[u], v[u][e], acc[e]);
     }
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < NS; ++u)
+    if (32 * u < 2 * k) add(x[u], 32 * u);
+  for (int i0 = 32 * NS; i0 < 2 * k; i0 += 32) add(i0 + lane < 2 * k ? __ldcg(pml + slot0 + i0 + lane) : make_float2(kNoMax, 0.f), i0);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
 #pragma unroll
