@@ -394,7 +394,8 @@ def lvq_plan_compaction(n_pages, order) -> CompactionPlan:
 
 
 def lvq_compact_pages(cfg, lay, plan: CompactionPlan, page_table, idx, dev_status, stream=None):
-    """Carries out a compaction plan in place on the pool's codes and rewrites the page table."""
+    """Carries out a compaction plan in place on the pool's codes and rewrites the page table.  Not under
+    capture: a plan belongs to one state of the pool, a replay would apply it to another."""
     if plan.n_pages != cfg.pool_pages:
         raise ValueError(f"the plan is for a pool of {plan.n_pages} pages, the configuration has {cfg.pool_pages}")
     dev, raw = torch.cuda.current_device(), _stream(stream)
@@ -402,6 +403,8 @@ def lvq_compact_pages(cfg, lay, plan: CompactionPlan, page_table, idx, dev_statu
     status = _on(dev, dev_status, "dev_status", torch.int32, 4)
     side = torch.cuda.stream(torch.cuda.ExternalStream(raw, device=dev)) if stream is not None else contextlib.nullcontext()
     with side:                                  # (the plan's device copy belongs to the call's stream)
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("lvq_compact_pages cannot be captured: a plan belongs to one state of the pool")
         on_device = plan._host.cuda(non_blocking=True)
         base = on_device.data_ptr()
         _check(lib().lvq_compact_pages(ctypes.byref(cfg), ctypes.byref(lay), plan.n_moves, base, base + 4 * plan._room,

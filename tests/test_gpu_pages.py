@@ -272,3 +272,45 @@ def test_serving_with_forks():
     for b in range(4):
         c.release(b)
     assert c.pool.available() == 150
+
+
+def test_captured_calls():
+    """Copies and forks replay on what the buffers hold then; a compaction is refused and leaves the pool as it was."""
+    w, cfg, c = _cache(1, 60, batch=4, n_recent=12, n_sink=3)
+    other = _cache(1, 60, batch=4)[2]
+    other.assign_pages(0, 3), other.assign_pages(1, 6)
+    other.release(0)
+    c.assign_pages(0, 6)
+    c.ctx_len[0], c.coded_len[0] = w.n_sink + 43 + 4, 43
+    tails = c.pool.alloc(2)
+    pairs = torch.tensor([[1, 50], [2, 51]], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lvq.lvq_copy_pages(cfg, c.lay, pairs, c.idx, c.status)
+        lvq.lvq_fork_requests(cfg, c.lay, 0, [2, 3], 43, tails, c.ctx_len, c.coded_len, c.sink, c.ring, c.idx,
+                              c.page_table, c.status)
+        with pytest.raises(RuntimeError, match="captured"):
+            other.compact()
+    assert other.pages[1] == list(range(3, 9)) and [other.pool.holders(p) for p in (0, 2, 3, 8, 9)] == [0, 0, 1, 1, 0]
+    stride = c.lay.page_table_stride
+    for seed in (1, 2):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        c.idx.random_(0, 256, generator=g)
+        c.ring.copy_(torch.randn(c.ring.shape, generator=g, device="cuda"))
+        pairs.copy_(torch.tensor([[seed, 50], [2, 51 + seed]], dtype=torch.int32))
+        c.ctx_len[2:] = 0
+        ref, ring = c.idx_view().clone(), c.ring_view().clone()
+        ref[:, :, :, :, 50], ref[:, :, :, :, 51 + seed] = ref[:, :, :, :, seed], ref[:, :, :, :, 2]
+        for ch, p in zip((2, 3), tails):
+            ref[:, :, :, :, p] = ref[:, :, :, :, 5]
+            for t in range(4):
+                ring[:, :, :, ch, :, (43 + t) % c.lay.ring_tokens] = ring[:, :, :, 0, :, (43 + t) % c.lay.ring_tokens]
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check_status()
+        assert torch.equal(c.idx_view(), ref) and torch.equal(c.ring_view(), ring)
+        assert c.ctx_len.tolist()[2:] == [w.n_sink + 47] * 2 and c.coded_len.tolist()[2:] == [43] * 2
+        for ch, p in zip((2, 3), tails):
+            assert c.page_table[ch * stride:ch * stride + 6].tolist() == [0, 1, 2, 3, 4, p]
