@@ -196,6 +196,10 @@ struct Sh {
   static constexpr int NI = NP / 4;                // pair-groups of a lane: P = quad + 4 i
   static constexpr int NW = D / 16;                // frequency pairs of a lane; k16 steps of a score
   static constexpr int NT = D / 8;                 // n8 tiles of an output row
+  // Shared entries of 8 channels or more: a tile's second page is scored against queries turned 8 positions back, so
+  // that a key's rotation moves on once a tile (32 behind 32K at c = 8: 152 us against 159; at c = 4, where the
+  // loads of smaller entries leave the loop less to save, 79 against 74)
+  static constexpr bool BACK = C >= 8;
   static constexpr int PAGE = NG * kPage;          // bytes of one K (or V) page
   static constexpr int STAGE = 4 * PAGE;           // a tile's codes: K pages, V pages
   static constexpr int KS = kEntries * D * 2;      // a step slice
@@ -211,7 +215,7 @@ struct Sh {
   static constexpr int OFF_Q = OFF_W + kWarps * WARP;
   static constexpr int OFF_F = OFF_Q + 2 * NW * 32 * 16;
   static constexpr int OFF_E = OFF_F + NW * 32 * 16;
-  static constexpr int OFF_R = OFF_E + NW * 4 * 16;
+  static constexpr int OFF_R = OFF_E + 2 * NW * 4 * 16;
   static constexpr int OFF_ML = OFF_R + kWarps * F * 8;
   static constexpr int OFF_INV = OFF_ML + kWarps * kQT * 8;
   static constexpr int OFF_RED = OFF_INV + kQT * 4;
@@ -307,7 +311,7 @@ template <int D, int C>
 struct Book {
   const unsigned char *Ks, *Vs;         // step slices: keys bf16, values scaled fp16 in padded rows
   const float4* Ff;                     // [frequency pair][lane]: (cos, cos, sin, sin) at (S % 8 + j)
-  const float4* E8;                     // [frequency pair][quad]: e^{i 8 theta}, (cos, cos, sin, sin)
+  const float4* E8;                     // [frequency pair][quad]: e^{i 8 theta}, (cos, cos, sin, sin); then e^{i 16 theta}
   float ks, kinv;                       // key scale (a power of two) and its reciprocal
 };
 
@@ -379,16 +383,18 @@ __device__ inline void add_values(float (&o)[4], const uint32_t (&ph)[4], const 
 // Query fragments: qf in registers (stacked rows), or qs in shared memory, [hi, lo][k step] 32 lanes apart.
 template <int D, int C, bool STK>
 __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, const Book<D, C>& bk, Run& run, State<D, C>& st,
-                                          const uint32_t (&qf)[Sh<D, C>::NW][4], const uint4* qs, const float (&qinv)[2],
+                                          const uint32_t (&qf)[Sh<D, C>::NW][4], const uint4* qs, const uint4* qs1, const float (&qinv)[2],
                                           unsigned char* stages, float4* rrow) {
   using X = Sh<D, C>;
   const int lane = threadIdx.x & 31, quad = lane & 3, row = lane >> 2;
   const int nt = ceil_div(run.n, kTT);
   const uint32_t vs0 = smem_addr(bk.Vs);
-  const float inv[2] = {qinv[0] * bk.kinv, qinv[1] * bk.kinv};
+  // (never zero: a masked score is -infinity times it)
+  const float inv[2] = {fmaxf(qinv[0] * bk.kinv, 1.17549435e-38f), fmaxf(qinv[1] * bk.kinv, 1.17549435e-38f)};
   // (queries and e^{i 8 theta} come from shared memory at every use: held in registers, they left the tile's loads and
   // products too few to overlap -- 161 us against 178 for 32 requests behind 32K tokens)
-  const float4* e8 = bk.E8 + quad;
+  constexpr bool BACK = X::BACK && !STK;
+  const float4* e8 = bk.E8 + quad + (BACK ? X::NW * 4 : 0);
   float2 wc[X::NW], ws[X::NW];
   for (int t = 0; t < nt; ++t) {
     cp_wait<X::NST - 2>();
@@ -430,16 +436,16 @@ __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, con
 #pragma unroll
         for (int v = 0; v < (C < 8 ? C / 2 : 4); ++v) {
           const int w = i * (C / 2) + q * 4 + v;
-          uint32_t qh[4];
-          if constexpr (STK) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) qh[k] = qf[w][k];
-          } else {
-            const uint4 x = qs[w * 32];
-            qh[0] = x.x; qh[1] = x.y; qh[2] = x.z; qh[3] = x.w;
-          }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
+            uint32_t qh[4];
+            if constexpr (STK) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) qh[k] = qf[w][k];
+            } else {
+              const uint4 x = BACK && u ? qs1[w * (X::WARP / 16)] : qs[w * 32];
+              qh[0] = x.x; qh[1] = x.y; qh[2] = x.z; qh[3] = x.w;
+            }
             const float2 kx = b2_lohi(lo[u][v]), ky = b2_lohi(hi[u][v]), c = wc[w], s = ws[w];
             // (scalar where a sign changes: packed operands have none to spare)
             const float2 r = make_float2(kx.x * c.x - ky.x * s.x, kx.y * c.y - ky.y * s.y);
@@ -449,14 +455,16 @@ __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, con
             split_h2(z, zh, zl);
             mma_f16(sl[u], qh, rl, zl);
             if constexpr (!STK) {
-              const uint4 x = qs[(X::NW + w) * 32];
+              const uint4 x = BACK && u ? qs1[w * (X::WARP / 16) + 32] : qs[(X::NW + w) * 32];
               const uint32_t ql[4] = {x.x, x.y, x.z, x.w};
               mma_f16(sl[u], ql, rh, zh);
             }
             mma_f16(sh[u], qh, rh, zh);
-            const float4 e = e8[w * 4];
-            wc[w] = make_float2(c.x * e.x - s.x * e.z, c.y * e.y - s.y * e.w);
-            ws[w] = __ffma2_rn(s, make_float2(e.x, e.y), __fmul2_rn(c, make_float2(e.z, e.w)));
+            if (!BACK || u) {
+              const float4 e = e8[w * 4];
+              wc[w] = make_float2(c.x * e.x - s.x * e.z, c.y * e.y - s.y * e.w);
+              ws[w] = __ffma2_rn(s, make_float2(e.x, e.y), __fmul2_rn(c, make_float2(e.z, e.w)));
+            }
           }
         }
       }
@@ -464,33 +472,31 @@ __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, con
     // ---- scores -> weights: column 2 quad + k of page u; masked past the run's last token
     constexpr int NR = STK ? 1 : 2;
     const int n = min(kTT, run.n - t * kTT);
-    float s[NR][2][2];                                               // [row][page][k]
+    float2 s[NR][2];                                                 // [row][page], times 1 / inv
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float v = sh[u][2 * r + k] + sl[u][2 * r + k];
-          if constexpr (STK) v += sh[u][2 + k] + sl[u][2 + k];
-          s[r][u][k] = v * inv[r];
-        }
+      for (int u = 0; u < 2; ++u) {
+        s[r][u] = __fadd2_rn(make_float2(sh[u][2 * r], sh[u][2 * r + 1]), make_float2(sl[u][2 * r], sl[u][2 * r + 1]));
+        if constexpr (STK) s[r][u] = __fadd2_rn(s[r][u], __fadd2_rn(make_float2(sh[u][2], sh[u][3]), make_float2(sl[u][2], sl[u][3])));
+      }
     if (n < kTT) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (8 * u + 2 * quad + k >= n)
-#pragma unroll
-            for (int r = 0; r < NR; ++r) s[r][u][k] = -INFINITY;
+        for (int r = 0; r < NR; ++r) {
+          if (8 * u + 2 * quad >= n) s[r][u].x = -INFINITY;
+          if (8 * u + 2 * quad + 1 >= n) s[r][u].y = -INFINITY;
+        }
     }
     float top[NR];
     bool grow = false;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      top[r] = fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][1][0], s[r][1][1]));
+      top[r] = fmaxf(fmaxf(s[r][0].x, s[r][0].y), fmaxf(s[r][1].x, s[r][1].y));
       top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
       top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+      top[r] *= inv[r];
       grow = grow || top[r] > st.m[r] + 14.f;
     }
     // outputs are rescaled only when a row outgrows its reference by 2^14, so that weights stay within fp16
@@ -512,7 +518,8 @@ __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, con
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const float2 p = make_float2(ex2(s[r][u][0] - st.m[r]), ex2(s[r][u][1] - st.m[r]));
+        const float2 d = __ffma2_rn(s[r][u], make_float2(inv[r], inv[r]), make_float2(-st.m[r], -st.m[r]));   // (inv is a power of two)
+        const float2 p = make_float2(ex2(d.x), ex2(d.y));
         st.l[r] += p.x + p.y;
         if constexpr (STK) split_h2(p, ph[2 * u], ph[2 * u + 1]);
         else split_h2(p, ph[2 * u + r], pl[2 * u + r]);
@@ -822,7 +829,10 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
     const int p = (g.S & 7) + row;
     const float4 x = __ldcg(rope4 + (size_t)(p >> 3) * (X::F / 2) + pair_of(warp));
     const float4 y = __ldcg(rope4 + (size_t)(g.RC + (p & 7)) * (X::F / 2) + pair_of(warp));
-    if (row == 0) E8[warp * 4 + quad] = make_float4(e.x, e.z, e.y, e.w);
+    if (row == 0) {
+      E8[warp * 4 + quad] = make_float4(e.x, e.z, e.y, e.w);
+      E8[(X::NW + warp) * 4 + quad] = make_float4(e.x * e.x - e.y * e.y, e.z * e.z - e.w * e.w, 2.f * e.x * e.y, 2.f * e.z * e.w);
+    }
     Ff[warp * 32 + lane] = make_float4(x.x * y.x - x.y * y.y, x.z * y.z - x.w * y.w, x.x * y.y + x.y * y.x, x.z * y.w + x.w * y.z);
   }
   const float qk_scale = 1.4426950408889634f / sqrtf((float)D);
@@ -831,6 +841,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
     uint4* Qf = reinterpret_cast<uint4*>(sm + X::OFF_Q);       // [hi, lo][k step][lane]
     constexpr int LPR = D / 4, RPW = 32 / LPR;                 // lanes of a row, rows a warp takes at once
     const int f2 = lane % LPR, P = 2 * f2 / C, sub = 2 * f2 % C / 2;
+    const float4 e = __ldcg(rope4 + X::F / 2 + f2);            // e^{i 8 theta}
 #pragma unroll 2
     for (int r = warp * RPW + lane / LPR; r < kQT; r += kWarps * RPW) {
       const bool live = r < rt.nrows && c.ctx[rt.request(r)] > 0;
@@ -838,14 +849,23 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
       float inv;
       query_pair<D>(g, a, live ? a.q + ((size_t)rt.request(r) * g.Hq + rt.head(r)) * D : a.q, live ? c.ctx[rt.request(r)] - 1 : 0, f2,
                     qk_scale, live, x, y, &inv);
-      uint32_t xh, xl, yh, yl;
-      split_h2(x, xh, xl);
-      split_h2(y, yh, yl);
       const int ks = P / 4 * (C / 2) + sub, fl = (r & 7) * 4 + P % 4, rg = r >> 3;
-      uint32_t* fh = reinterpret_cast<uint32_t*>(Qf + ks * 32 + fl);
-      uint32_t* fw = reinterpret_cast<uint32_t*>(Qf + (X::NW + ks) * 32 + fl);
-      fh[rg] = xh; fh[rg + 2] = yh;
-      fw[rg] = xl; fw[rg + 2] = yl;
+      auto put = [&](uint4* hi, uint4* lo) {
+        uint32_t xh, xl, yh, yl;
+        split_h2(x, xh, xl);
+        split_h2(y, yh, yl);
+        uint32_t *fh = reinterpret_cast<uint32_t*>(hi + fl), *fw = reinterpret_cast<uint32_t*>(lo + fl);
+        fh[rg] = xh; fh[rg + 2] = yh;
+        fw[rg] = xl; fw[rg + 2] = yl;
+      };
+      put(Qf + ks * 32, Qf + (X::NW + ks) * 32);
+      if constexpr (X::BACK) {                                 // and turned 8 positions back, in the warps' areas
+        const float2 b = make_float2(x.x * e.x + y.x * e.y, x.y * e.z + y.y * e.w);
+        y = make_float2(y.x * e.x - x.x * e.y, y.y * e.z - x.y * e.w);
+        x = b;
+        uint4* Q1 = reinterpret_cast<uint4*>(sm + X::OFF_W + ks * X::WARP + X::PARK);
+        put(Q1, Q1 + 32);
+      }
       if (f2 == 0) inv_s[r] = inv;
     }
   };
@@ -971,7 +991,9 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
       State<D, C> st;
       st.clear();
       const uint32_t none[X::NW][4] = {};
-      if (run.n > 0) coded_run<D, C, false>(g, a, bk, run, st, none, reinterpret_cast<const uint4*>(sm + X::OFF_Q) + lane, qinv, area, rrow);
+      if (run.n > 0) coded_run<D, C, false>(g, a, bk, run, st, none, reinterpret_cast<const uint4*>(sm + X::OFF_Q) + lane,
+                                               reinterpret_cast<const uint4*>(sm + X::OFF_W + X::PARK) + lane, qinv, area, rrow);
+      if constexpr (X::BACK) __syncthreads();                  // (queries lie in the areas)
       // the warps' results are joined
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -1010,9 +1032,12 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
         }
       }
       next_tile(false);
-      if (e < a.ng) set_queries(rt);                           // (every warp is past reading the last ones)
-      __syncthreads();
-      if (e < a.ng) start_shared();                            // (and the areas are read)
+      __syncthreads();                                         // the areas are read
+      if (e < a.ng) {
+        start_shared();
+        set_queries(rt);
+        __syncthreads();
+      }
     }
   }
 
@@ -1083,7 +1108,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
           State<D, C> st;
           st.clear();
           if (!small) begin_run<D, C>(g, a, run, area, rrow);
-          coded_run<D, C, true>(g, a, bk, run, st, qf, nullptr, qinv, area, rrow);
+          coded_run<D, C, true>(g, a, bk, run, st, qf, nullptr, nullptr, qinv, area, rrow);
           st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], 1);
           st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], 2);
           if (row < nrows) {
