@@ -28,9 +28,11 @@ constexpr int kQT = 16;                 // query rows of a tile of shared tokens
 constexpr int kOT = 8;                  // query heads of a tile of own tokens
 constexpr int kTT = 16;                 // tokens of a tile: two pages
 // Costs in token tiles: a query tile of a shared entry as such (fragments, joining the warps), one of an own entry, and
-// what the first part with own entries spends on getting to them.  Swept one after the other over 22 shapes to their
-// least geometric mean, 32.0 us (33.2 without the last one).
-constexpr int kSharedCost = 8, kOwnCost = 4, kOwnStage = 20;
+// what the first part with own entries spends on getting to them; and what a tile of own tokens weighs against a
+// shared one (its bytes are new to L2, and its warps wait for more of them).  Swept one after the other over 64 shapes
+// whose inputs L2 does not hold to their least geometric mean: 32.1 us (32.5 with both tiles alike and a stage of 20).
+constexpr int kSharedCost = 8, kOwnCost = 4, kOwnStage = 40;
+constexpr int kSharedWeight = 8, kOwnWeight = 9;
 constexpr int kWarps = 8;
 constexpr int kShThreads = 32 * kWarps;
 constexpr float kNoMax = -1e30f;        // softmax reference before the first token
@@ -871,8 +873,9 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   };
   // this part of the head's list: [cut0, cut1), shared entries first; e, qt: where it begins
   const long long shared_total = ok ? c.gcum[a.ng] : 0, own_total = ok ? c.ocum[a.batch] : 0;
-  const long long own_at = shared_total + (shared_total > 0 && own_total > 0 ? kOwnStage : 0), total = own_at + own_total;
-  const long long cut0 = div_cost(total * j, a.k), cut1 = div_cost(total * (j + 1), a.k);
+  const long long own_at = shared_total * kSharedWeight + (shared_total > 0 && own_total > 0 ? kOwnStage * kSharedWeight : 0);
+  const long long total = own_at + own_total * kOwnWeight, at0 = div_cost(total * j, a.k), at1 = div_cost(total * (j + 1), a.k);
+  const long long cut0 = min(shared_total, at0 / kSharedWeight), cut1 = min(shared_total, at1 / kSharedWeight);
   int e = a.ng, qt = 0;
   Entry en = {0, 0, 0, 0, 1};
   RowTile rt;
@@ -1042,7 +1045,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   }
 
   // ---- own entries: a contiguous run of the part's tiles to a warp
-  const long long o0 = max(0ll, cut0 - own_at), o1 = max(0ll, cut1 - own_at);
+  const long long o0 = div_cost(max(0ll, at0 - own_at), kOwnWeight), o1 = div_cost(max(0ll, at1 - own_at), kOwnWeight);
   if (o0 >= o1) return;
   const long long x0 = o0 + (o1 - o0) * warp / kWarps, x1 = o0 + (o1 - o0) * (warp + 1) / kWarps;
   int* park_s = reinterpret_cast<int*>(red) + 2 * kWarps;      // [warp]: entry tile whose beginning another warp has, or -1
