@@ -208,7 +208,8 @@ struct Sh {
   static constexpr int VROW = D * 2 + 16;          // a padded row of the value slice
   static constexpr int OROW = D + 4;               // a padded row of a warp's output, in floats
   // a warp's area: code stages, a query tile's fragments or 8 output rows, then 8 output rows parked
-  // (a shared entry's 16 output rows take both)
+  // (a shared entry's 16 output rows take both; before them, the parked rows' place of area w holds k step w of the
+  // queries turned back)
   static constexpr int WARP = kQT * OROW * 4;
   static constexpr int PARK = kOT * OROW * 4;
   static constexpr int NST = PARK / STAGE < 6 ? PARK / STAGE : 6;
@@ -227,7 +228,7 @@ struct Sh {
   static constexpr int smem(int batch, int ng) { return OFF_C + counter_bytes(batch, ng); }
   static_assert(NP % 4 == 0 && NI * C == 2 * NW, "lane mapping");
   static_assert(NST >= 3 && NST <= 8, "stages (a tile's RoPE row is read before the one 8 tiles on is fetched)");
-  static_assert(PARK >= NW * 32 * 16, "the warps' areas");
+  static_assert(PARK >= NW * 32 * 16 && WARP - PARK >= 2 * 32 * 16 && NW <= kWarps, "the warps' areas");
   static_assert(OFF_C + counter_bytes(kSharedMaxBatch, kSharedMaxBatch) <= 227 * 1024, "shared memory");
   static_assert(OFF_W % 16 == 0 && PARK % 16 == 0 && OFF_F % 16 == 0 && OFF_BAR % 8 == 0 && OFF_C % 8 == 0, "alignment");
 };
@@ -379,10 +380,11 @@ __device__ inline void add_values(float (&o)[4], const uint32_t (&ph)[4], const 
 // (j, quad) restores token j of each of the two pages: the entries of pair-groups P = quad + 4 i straight
 // into the B fragments of mma.sync m16n8k16 (the order of a dot product's channels is free, so a fragment's k
 // indices are the channels of the lane's own entries), rotated in fp32 by e^{i p theta}, which moves on by a
-// page (8 positions) with one complex multiplication and is taken anew from the tables every 16 pages.  Keys
-// and queries enter as sums of two fp16 values, good to 2^-22 of the largest; lo x lo is left out of 16 rows.
-// Weights too are sums of two fp16 values; values are exact.
-// Query fragments: qf in registers (stacked rows), or qs in shared memory, [hi, lo][k step] 32 lanes apart.
+// page (8 positions; Sh::BACK: by two) with one complex multiplication and is taken anew from the tables every
+// 16 pages.  Keys and queries enter as sums of two fp16 values, good to 2^-22 of the largest; lo x lo is left
+// out of 16 rows.  Weights too are sums of two fp16 values; values are exact.
+// Query fragments: qf in registers (stacked rows), or qs in shared memory, [hi, lo][k step] 32 lanes apart
+// (qs1: turned back for a tile's second page, [k step][hi, lo]).
 template <int D, int C, bool STK>
 __device__ __forceinline__ void coded_run(const Geo& g, const SharedArgs& a, const Book<D, C>& bk, Run& run, State<D, C>& st,
                                           const uint32_t (&qf)[Sh<D, C>::NW][4], const uint4* qs, const uint4* qs1, const float (&qinv)[2],
@@ -764,10 +766,13 @@ __device__ __forceinline__ void query_pair(const Geo& g, const SharedArgs& a, co
 // rows padded by 16 bytes (8 tokens' entries of one group then fall on different banks as often as not).
 //
 // What bounds it.  The bytes are few (32 requests behind 32K tokens at c = 8: 60.6 MB, 9.2 us); restoring, rotating and
-// splitting a key is some 30 warp instructions a token and 16 rows, products 5 (10.6 cycles of the SM's mma.sync
-// pipe), the rest weights, values and loads: 57 in all.  At 255 registers two warps share a scheduler, which issues
-// 0.36 a cycle (counters: fixed latencies 0.95, pipe throttle 0.72, instruction fetch 0.56, shared memory 0.53 cycles
-// of stall an instruction): 28 cycles a token and 16 rows, 161 us for those 32 requests on an idle stream.
+// splitting a key is some 28 warp instructions a token and 16 rows, products 5 (10.6 cycles of the SM's mma.sync
+// pipe), the rest weights, values and loads: 55 in all.  At 255 registers two warps share a scheduler, which issues
+// 0.36 a cycle (counters: fixed latencies 0.98, shared memory 0.74, pipe throttle 0.63, instruction fetch 0.51 cycles
+// of stall an instruction): 27 cycles a token and 16 rows, 157 us for those 32 requests replayed, 163 us with inputs
+// that L2 does not hold.  No part of the loop bounds it by itself: without the products of the keys' or the queries'
+// low parts it takes 6 or 4 % less, without bank conflicts on values 5 %; keys laid out for half their conflicts
+// gained 1 %, less than laying them out cost.
 // Tried and slower: 12 warps of 168 registers (spills: 214 us), values of one tile beside the scores of the next (167
 // to 178), two row tiles to one restored key (156 to 173, and 99 against 86 for 64K with four heads a KV head), and
 // tcgen05 products of 32 rows fed by restoring warps through swizzled shared memory (219 us: M = 128 tiles of 64
