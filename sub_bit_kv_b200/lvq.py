@@ -7,6 +7,7 @@ fallback path.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import functools
@@ -188,8 +189,13 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, min_bytes: int = 0, o
     return t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:             # the same handle without a Stream object: 0.3 us instead of 3.2
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -357,15 +363,19 @@ class CompactionPlan:
     moves for lvq_compact_pages (host int32 [n_moves][2])."""
 
     def __init__(self, n_pages: int, order):
-        order = torch.as_tensor(order, dtype=torch.int32, device="cpu").contiguous()
-        n = order.numel()
+        if isinstance(order, torch.Tensor):
+            order = order.to(device="cpu", dtype=torch.int32).contiguous()
+            n, ids = order.numel(), order.data_ptr()
+        else:
+            order = array.array("i", order)     # (a quarter of the time that a tensor takes from a list)
+            n, ids = len(order), order.buffer_info()[0]
         self.n_pages = int(n_pages)
         # one buffer, so that it goes to the device in one copy: the moves, then new_id
         self._room = 2 * (n + n // 2)
         self._host = torch.empty(self._room + max(1, self.n_pages), dtype=torch.int32, pin_memory=_has_cuda())
         k = _I32()
         base = self._host.data_ptr()
-        _check(lib().lvq_plan_compaction(self.n_pages, order.data_ptr() if n else None, n, base + 4 * self._room,
+        _check(lib().lvq_plan_compaction(self.n_pages, ids if n else None, n, base + 4 * self._room,
                                          base if n else None, ctypes.byref(k)), "lvq_plan_compaction")
         self.n_moves = k.value
 
