@@ -386,8 +386,9 @@ LVQ_API lvq_status lvq_compact_pages(const lvq_config* cfg, const lvq_layout* la
  * outside pool mode).
  * Device-side: LVQ_EINVAL in *dev_status if coded_len[parent] is not coded_tokens, LVQ_ECAPACITY
  * if the parent's counters are outside the layout or its partial page is not in the page table;
- * nothing is written then.  Slots of the window that hold no token, and requests that are not
- * named, stay as they are. */
+ * nothing is written then, and pages taken from an lvq_pool for the children go back to it
+ * (lvq_pool_free) once the status is known.  Slots of the window that hold no token, and requests
+ * that are not named, stay as they are. */
 LVQ_API lvq_status lvq_fork_requests(const lvq_config* cfg, const lvq_layout* lay, int32_t parent,
                                      int32_t n_children, const int32_t* children,
                                      int32_t coded_tokens, const int32_t* tail_pages,

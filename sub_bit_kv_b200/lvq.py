@@ -200,6 +200,13 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _current(stream):
+    """Makes the call's stream the current one for torch's own allocations and copies."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=torch.cuda.current_device()))
+
+
 def lvq_pack_codebooks(cfg, lay, cb, cbp, cb_norm=None, stream=None):
     _check(lib().lvq_pack_codebooks(
         ctypes.byref(cfg), ctypes.byref(lay), _ptr(cb, "cb", torch.bfloat16, lay.cb_bytes),
@@ -411,8 +418,7 @@ def lvq_compact_pages(cfg, lay, plan: CompactionPlan, page_table, idx, dev_statu
     dev, raw = torch.cuda.current_device(), _stream(stream)
     table, codes = _table(cfg, lay, dev, page_table), _on(dev, idx, "idx", torch.uint8, lay.idx_bytes)
     status = _on(dev, dev_status, "dev_status", torch.int32, 4)
-    side = torch.cuda.stream(torch.cuda.ExternalStream(raw, device=dev)) if stream is not None else contextlib.nullcontext()
-    with side:                                  # (the plan's device copy belongs to the call's stream)
+    with _current(stream):                      # (the plan's device copy belongs to the call's stream)
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("lvq_compact_pages cannot be captured: a plan belongs to one state of the pool")
         on_device = plan._host.cuda(non_blocking=True)
@@ -493,12 +499,19 @@ class CodedCache:
             self.pages[b] = []
             self.page_table[b * self.lay.page_table_stride:(b + 1) * self.lay.page_table_stride].fill_(-1)
 
-    def fork(self, parent: int, children, coded_tokens: int, stream=None) -> None:
+    def fork(self, parent: int, children, coded_tokens: int, stream=None, check: bool = False) -> None:
         """Every request of `children` becomes a copy of request `parent`, which has coded_tokens coded
         tokens.  In pool mode the children hold the parent's full pages with it and get a page of their
-        own for a partial last one; they must hold no pages before."""
+        own for a partial last one; they must hold no pages before.
+
+        The call does not wait: the children's page lists are filled on the caller's word.  Where the device
+        finds otherwise (coded_len[parent] is not coded_tokens, the parent's counters or its partial page are
+        bad), it writes the status and no child, and every child has to be released before it, assign_pages
+        or compact is used on.  check=True waits for the fork and, refused, gives the pages back and raises
+        LvqError (it reads a status word of its own; not under capture)."""
         children = list(children)
         tails = None
+        status = self.status
         if self.pool is not None:
             if any(self.pages[c] for c in children):
                 raise ValueError("a child holds pages: release it first")
@@ -508,8 +521,15 @@ class CodedCache:
             if rest:
                 tails = self.pool.alloc(len(children))
         try:
-            lvq_fork_requests(self.cfg, self.lay, parent, children, coded_tokens, tails, self.ctx_len, self.coded_len,
-                              self.sink, self.ring, self.idx, getattr(self, "page_table", None), self.status, stream)
+            with _current(stream) if check else contextlib.nullcontext():
+                if check:
+                    if status.is_cuda and torch.cuda.is_current_stream_capturing():
+                        raise RuntimeError("a captured fork cannot be checked")
+                    status = torch.zeros_like(status)
+                lvq_fork_requests(self.cfg, self.lay, parent, children, coded_tokens, tails, self.ctx_len, self.coded_len,
+                                  self.sink, self.ring, self.idx, getattr(self, "page_table", None), status, stream)
+                if check:
+                    _check(int(status.item()), "lvq_fork_requests")
         except Exception:
             if tails:
                 self.pool.free(tails)
