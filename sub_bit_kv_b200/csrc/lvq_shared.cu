@@ -35,7 +35,7 @@ constexpr int kSharedCost = 8, kOwnCost = 4, kOwnStage = 40;
 constexpr int kSharedWeight = 8, kOwnWeight = 9;
 constexpr int kWarps = 8;
 constexpr int kShThreads = 32 * kWarps;
-constexpr float kNoMax = -1e30f;        // softmax reference before the first token
+constexpr float kNoMax = -3.40282347e38f;   // softmax reference before the first token: the lowest float, which no score is below
 
 struct SharedArgs {
   int layer, step, batch, ng, k;
