@@ -410,7 +410,9 @@ LVQ_API lvq_status lvq_fork_requests(const lvq_config* cfg, const lvq_layout* la
  *   num_splits: every KV head's work is cut into num_splits parts of equal cost, a CTA each
  *     (1 .. max_splits); 0 lets the library choose.
  *   workspace: as for lvq_decode_attention, whose calls may share it (its counters stay zero).
- * Other arguments as for lvq_decode_attention.  batch <= 256, else LVQ_EUNSUPPORTED.  Sums are
+ * Other arguments as for lvq_decode_attention.  LVQ_EUNSUPPORTED: batch above 256, and in pool
+ * mode max_pages / (num_splits n_kv_heads) x (batch - 1) above 2^30 (page-table entries that one
+ * CTA compares; with 255 other requests, 33 million tokens in one part of one head).  Sums are
  * taken in a fixed order: the same call gives the same bits.  A request whose counters are
  * outside the layout (its rows come out as 0, lse -inf), or page-table entries out of range:
  * LVQ_ECAPACITY, as there; a group_begin that is not as described: LVQ_EINVAL (outputs then not

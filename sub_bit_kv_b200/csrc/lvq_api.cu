@@ -305,6 +305,7 @@ lvq_status lvq_decode_attention_shared(const lvq_config* cfg, const lvq_layout* 
       num_splits > g.max_splits || n_groups < 0 || n_groups > batch || (batch > 0 && n_groups == 0))
     return LVQ_EINVAL;
   if (batch > kSharedMaxBatch) return LVQ_EUNSUPPORTED;
+  if (num_splits > 0 && !shared_rows_countable(g, batch, num_splits)) return LVQ_EUNSUPPORTED;
   if (batch > 0) {
     const void* ptrs[] = {q, ring, idx, cbp, rope, workspace, out, lse};
     for (const void* p : ptrs)
@@ -316,11 +317,13 @@ lvq_status lvq_decode_attention_shared(const lvq_config* cfg, const lvq_layout* 
   if (batch == 0) return LVQ_OK;
   const int n_sm = device_sms();
   if (n_sm < 1) return LVQ_ECUDA;
+  const int parts = num_splits > 0 ? num_splits : shared_parts(g, batch, n_sm);
+  if (!shared_rows_countable(g, batch, parts)) return LVQ_EUNSUPPORTED;
   return cuda_status(launch_decode_shared(g, layer, step, batch, static_cast<const __nv_bfloat16*>(q), ctx_len, coded_len,
                                           n_groups, group_begin, group_tokens, static_cast<const __nv_bfloat16*>(sink),
                                           static_cast<const __nv_bfloat16*>(ring), idx,
-                                          static_cast<const __nv_bfloat16*>(cbp), rope, num_splits, workspace, out, lse,
-                                          dev_status, n_sm, static_cast<cudaStream_t>(stream)));
+                                          static_cast<const __nv_bfloat16*>(cbp), rope, parts, workspace, out, lse,
+                                          dev_status, static_cast<cudaStream_t>(stream)));
 }
 
 lvq_status lvq_copy_pages(const lvq_config* cfg, const lvq_layout* lay, int32_t n, const int32_t* pairs, uint8_t* idx,

@@ -199,10 +199,12 @@ cudaError_t launch_fork(const Geo& g, int parent, int n, const int32_t* children
                         int32_t* ctx_len, int32_t* coded_len, __nv_bfloat16* sink, __nv_bfloat16* ring, uint8_t* idx,
                         int32_t* table, int32_t* st, cudaStream_t s);
 constexpr int kSharedMaxBatch = 256;    // requests one lvq_decode_attention_shared call can take
+int shared_parts(const Geo& g, int batch, int n_sm);                  // parts a KV head where the caller names none
+bool shared_rows_countable(const Geo& g, int batch, int k);
 cudaError_t launch_decode_shared(const Geo& g, int layer, int step, int batch, const __nv_bfloat16* q,
                                  const int32_t* ctx_len, const int32_t* coded_len, int n_groups,
                                  const int32_t* group_begin, const int32_t* group_tokens, const __nv_bfloat16* sink,
                                  const __nv_bfloat16* ring, const uint8_t* idx, const __nv_bfloat16* cbp,
-                                 const float* rope, int num_splits, float* ws, float* out, float* lse, int32_t* st,
-                                 int n_sm, cudaStream_t s);
+                                 const float* rope, int k, float* ws, float* out, float* lse, int32_t* st,
+                                 cudaStream_t s);
 }  // namespace lvq

@@ -164,7 +164,8 @@ __device__ bool load_counters(const Geo& g, const SharedArgs& a, Counters& c, lo
   return true;
 }
 
-// Pool mode: the rows of a group name the same pages for its shared tokens.  The CTAs share the comparison.
+// Pool mode: the rows of a group name the same pages for its shared tokens.  The CTAs share the comparison (an int
+// counts a CTA's: calls that need more are refused).
 __device__ void check_rows(const Geo& g, const SharedArgs& a, const Counters& c) {
   const int n_cta = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
   bool differ = false;
@@ -1290,24 +1291,30 @@ static cudaError_t shared_as(const Geo& g, SharedArgs a, float* out, float* lse,
   return cudaLaunchKernelEx(&lc, shared_merge_kernel<D>, g, rows, a.k, (const float*)a.po, (const float2*)a.pml, out, lse);
 }
 
+int shared_parts(const Geo& g, int batch, int n_sm) {
+  // one wave of CTAs; where the layout holds few tokens, two parts a request and two for the shared ones, or one to
+  // 128 tokens (two requests of 464 tokens, one head: 12.3 us with 9 parts, 15.5 with 64, 19.0 with one; four of 20
+  // tokens, 16 heads: 13.9 with 9, 18.2 with one)
+  const long long by_tokens = ((long long)batch * g.max_ctx + 127) / 128, by_batch = 2ll * batch + 2;
+  const long long most = by_tokens > by_batch ? by_tokens : by_batch;
+  int k = n_sm / g.H < 1 ? 1 : n_sm / g.H;
+  if (k > g.max_splits) k = g.max_splits;
+  if (k > most) k = (int)most;
+  return k;
+}
+
+bool shared_rows_countable(const Geo& g, int batch, int k) {
+  return !g.pool || (g.P / ((long long)k * g.H) + 1) * (batch - 1) <= 1 << 30;   // (check_rows)
+}
+
 cudaError_t launch_decode_shared(const Geo& g, int layer, int step, int batch, const __nv_bfloat16* q,
                                  const int32_t* ctx_len, const int32_t* coded_len, int n_groups,
                                  const int32_t* group_begin, const int32_t* group_tokens, const __nv_bfloat16* sink,
                                  const __nv_bfloat16* ring, const uint8_t* idx, const __nv_bfloat16* cbp,
-                                 const float* rope, int num_splits, float* ws, float* out, float* lse, int32_t* st,
-                                 int n_sm, cudaStream_t s) {
-  SharedArgs a = {layer, step, batch, n_groups, num_splits, q, ctx_len, coded_len, group_begin, group_tokens,
+                                 const float* rope, int k, float* ws, float* out, float* lse, int32_t* st,
+                                 cudaStream_t s) {
+  SharedArgs a = {layer, step, batch, n_groups, k, q, ctx_len, coded_len, group_begin, group_tokens,
                   sink, ring, idx, cbp, rope, ws, nullptr, st};
-  if (a.k == 0) {
-    // one wave of CTAs; where the layout holds few tokens, two parts a request and two for the shared ones, or one to
-    // 128 tokens (two requests of 464 tokens, one head: 12.3 us with 9 parts, 15.5 with 64, 19.0 with one; four of 20
-    // tokens, 16 heads: 13.9 with 9, 18.2 with one)
-    const long long by_tokens = ((long long)batch * g.max_ctx + 127) / 128, by_batch = 2ll * batch + 2;
-    const long long most = by_tokens > by_batch ? by_tokens : by_batch;
-    a.k = n_sm / g.H < 1 ? 1 : n_sm / g.H;
-    if (a.k > g.max_splits) a.k = g.max_splits;
-    if (a.k > most) a.k = (int)most;
-  }
   a.pml = reinterpret_cast<float2*>(ws + (size_t)g.B * g.Hq * g.max_splits * 2 * g.d);
   if (g.d == 128 && g.c == 4) return shared_as<128, 4>(g, a, out, lse, s);
   if (g.d == 128 && g.c == 8) return shared_as<128, 8>(g, a, out, lse, s);
