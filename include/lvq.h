@@ -170,7 +170,8 @@ LVQ_API const char* lvq_status_string(lvq_status s);
  * of the later calls gives up after `wait_iters` polls (<= 0: the normal bound, about 2^24)
  * and reports LVQ_ETIMEOUT in *dev_status; `fault_mask` makes a copy never happen, so that
  * such a wait runs out: bit 0 -- lvq_decode_attention skips the first code chunk of every
- * CTA; bit 1 -- lvq_kmeans_update skips the first tile of every CTA.  Kernels still wait
+ * CTA; bit 1 -- lvq_kmeans_update skips the first tile of every CTA; bit 2 --
+ * lvq_decode_attention_shared skips the values of every CTA.  Kernels still wait
  * (bounded) for every copy they did issue before they exit, so the context stays usable.
  * LVQ_EINVAL for unknown bits.  lvq_debug_faults(0, 0) restores normal operation. */
 LVQ_API lvq_status lvq_debug_faults(int64_t wait_iters, int32_t fault_mask);

@@ -384,7 +384,7 @@ lvq_status lvq_fork_requests(const lvq_config* cfg, const lvq_layout* lay, int32
 }
 
 lvq_status lvq_debug_faults(int64_t wait_iters, int32_t fault_mask) {
-  if (fault_mask & ~(kFaultDecodeDropChunk | kFaultKmeansDropTile)) return LVQ_EINVAL;
+  if (fault_mask & ~(kFaultDecodeDropChunk | kFaultKmeansDropTile | kFaultSharedDropSlice)) return LVQ_EINVAL;
   debug_wait_iters = wait_iters > 0 ? (long)wait_iters : kWaitIters;
   debug_fault = fault_mask;
   return LVQ_OK;

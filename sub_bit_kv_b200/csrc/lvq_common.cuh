@@ -30,6 +30,7 @@ struct Geo {
 // runs out and the kernel reports LVQ_ETIMEOUT.
 constexpr int kFaultDecodeDropChunk = 1;   // decode: the first code chunk of every CTA
 constexpr int kFaultKmeansDropTile = 2;    // k-means update: the first tile of every CTA
+constexpr int kFaultSharedDropSlice = 4;   // attention over shared prefixes: every CTA's value slice
 
 // byte offset of the code stream [page][n_g][8] of (layer, blk, b, h, kv)
 __host__ __device__ inline size_t idx_stream_off(const Geo& g, int layer, int blk, int b, int h, int kv) {

@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   if (tid == 0) {
     mbar_expect_tx(bar, 2 * X::KS);
     bulk_g2s(smem_addr(Ks), kslice, X::KS, bar);
-    bulk_g2s(smem_addr(Vs), vslice, X::KS, bar);
+    if (!(g.fault & kFaultSharedDropSlice)) bulk_g2s(smem_addr(Vs), vslice, X::KS, bar);
   }
   // every slot of this part starts empty
   for (int i = tid; i < a.batch * rep * 2; i += kShThreads) {
@@ -931,6 +931,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_kernel(Geo g, SharedArgs
   if (late || !ok) {
     if (late && tid == 0) {
       set_status(a.st, LVQ_ETIMEOUT);
+      if (g.fault & kFaultSharedDropSlice) bulk_g2s(smem_addr(Vs), vslice, X::KS, bar);   // (the barrier expects it)
       mbar_wait(bar, 0, kWaitIters);                           // the copies land before the CTA exits
     }
     cp_wait<0>();

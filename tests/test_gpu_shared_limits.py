@@ -1,4 +1,4 @@
-"""Attention over shared prefixes at the ends of its range: scores near the lowest float."""
+"""Attention over shared prefixes at the ends of its range: scores near the lowest float, waits that run out."""
 import dataclasses
 
 import numpy as np
@@ -59,3 +59,27 @@ def test_scores_near_the_lowest_float(name, over, tokens, coded, log2_q, log2_k)
                 assert rl < -2e32
                 assert np.abs(out[b, h].double().numpy() - ro).max() <= 2.0 ** -16 * np.abs(ro).max()
                 assert abs(float(lse[b, h]) - rl) <= 2.0 ** -18 * abs(rl)
+
+
+@pytest.mark.parametrize("name,over", [("tiny", {}), ("ouro14_g16_32k", {}), ("ouro14_g32_b32", {}), ("ouro14_tc1_32k", {})])
+def test_a_wait_that_runs_out(name, over):
+    """Every CTA's values never come: the call ends with LVQ_ETIMEOUT and empty rows, and the same context then
+    computes right results, this attention's and lvq_decode_attention's on the same workspace."""
+    w = dataclasses.replace(synth.WORKLOADS[name], n_layers=1, n_kv_heads=2, n_q_heads=4, **over)
+    case, begin, tokens = Sh.shared_case(w, [(300, [3, 200]), (0, [40])], recent=[7, 9, 11])
+    pcase = Sh.to_pool(case, begin, tokens)
+    q = synth.queries(w, 0, 1, batch=3).cuda()
+    ref, rl, _ = Hl.run_decode(pcase, 0, 1, q, 5, split_lse=False)
+    for ns in (0, 1, 7):
+        lvq.lvq_debug_faults(16, 4)
+        try:
+            out, lse = Sh.run_shared(pcase, begin, tokens, 1, q, num_splits=ns, check=False)
+        finally:
+            lvq.lvq_debug_faults(0, 0)
+        assert int(pcase.cache.status.item()) == lvq.LVQ_ETIMEOUT
+        pcase.cache.status.zero_()
+        assert (out == 0).all() and (lse == -float("inf")).all()
+        out, lse = Sh.run_shared(pcase, begin, tokens, 1, q, num_splits=ns)
+        Sh.check_against_oracle(case, 1, q, out, lse)
+        got, gl, _ = Hl.run_decode(pcase, 0, 1, q, 5, split_lse=False)
+        assert torch.equal(ref, got) and torch.equal(rl, gl)

@@ -33,3 +33,12 @@ def test_more_table_entries_than_a_cta_counts_are_refused():
         assert attend(256, 8) == lvq.LVQ_EDEVICE and attend(32, 1) == lvq.LVQ_EDEVICE and attend(256, 0) == lvq.LVQ_EDEVICE
         cfg.pool_pages, cfg.page_table = 0, None
         assert attend(256, 1, cfg, plain) == lvq.LVQ_EDEVICE               # no table, nothing to compare
+
+
+def test_fault_bits():
+    for mask in (8, 1 << 30, -1):
+        with pytest.raises(lvq.LvqError) as e:
+            lvq.lvq_debug_faults(0, mask)
+        assert e.value.status == lvq.LVQ_EINVAL
+    lvq.lvq_debug_faults(1 << 10, 7)
+    lvq.lvq_debug_faults(0, 0)
