@@ -399,7 +399,10 @@ LVQ_API lvq_status lvq_fork_requests(const lvq_config* cfg, const lvq_layout* la
 
 /* Decode attention of loop step `step` of layer `layer` for a batch whose requests share coded
  * prefixes: what lvq_decode_attention computes, with the shared tokens of a group of requests
- * read, restored and rotated once for all the group's queries.
+ * restored and rotated once for every 16 of the group's query rows (a row: a request's query head of
+ * the KV head).  For groups of two or more behind a prefix of some thousand tokens; a request that
+ * shares nothing, or a batch whose (request, query head) pairs are few, is served sooner by
+ * lvq_decode_attention.
  *   group_begin: device int32 [n_groups + 1], ascending from 0 to batch; group i holds the
  *     requests [group_begin[i], group_begin[i + 1]).  A request on its own is a group of one.
  *   group_tokens: device int32 [n_groups]: coded tokens 0 .. group_tokens[i] - 1 are the same in
@@ -409,7 +412,9 @@ LVQ_API lvq_status lvq_fork_requests(const lvq_config* cfg, const lvq_layout* la
  *     that does not sets LVQ_EINVAL in *dev_status.  Otherwise they are read from the group's
  *     first request.
  *   num_splits: every KV head's work is cut into num_splits parts of equal cost, a CTA each
- *     (1 .. max_splits); 0 lets the library choose.
+ *     (1 .. max_splits); 0 lets the library choose: one wave of CTAs, SMs / n_kv_heads parts (one
+ *     where there are more heads than half the SMs), but no more than max_splits -- a layout of one
+ *     KV head fills the device with max_splits >= 148 -- and fewer for small layouts.
  *   workspace: as for lvq_decode_attention, whose calls may share it (its counters stay zero).
  * Other arguments as for lvq_decode_attention.  LVQ_EUNSUPPORTED: batch above 256, and in pool
  * mode max_pages / (num_splits n_kv_heads) x (batch - 1) above 2^30 (page-table entries that one
@@ -417,8 +422,9 @@ LVQ_API lvq_status lvq_fork_requests(const lvq_config* cfg, const lvq_layout* la
  * taken in a fixed order: the same call gives the same bits.  A request whose counters are
  * outside the layout (its rows come out as 0, lse -inf), or page-table entries out of range:
  * LVQ_ECAPACITY, as there; a group_begin that is not as described: LVQ_EINVAL (outputs then not
- * meaningful).  Entries and tokens are scaled by powers of two to the head's largest finite entry,
- * beside which smaller ones keep 2^-39 of it (keys) and 2^-28 (values) as absolute precision. */
+ * meaningful).  Entries are scaled by powers of two to the head's largest finite one (of 2^-77 or
+ * more): keys enter with an error of at most 2^-22 of their size or 2^-38 of the largest, values
+ * no smaller than 2^-28 of the largest exactly. */
 LVQ_API lvq_status lvq_decode_attention_shared(const lvq_config* cfg, const lvq_layout* lay, int32_t layer,
                                                int32_t step, int32_t batch, const void* q,
                                                const int32_t* ctx_len, const int32_t* coded_len,

@@ -335,7 +335,7 @@ def lvq_decode_attention_shared(cfg, lay, layer, step, batch, q, ctx_len, coded_
                                 ring, idx, cbp, rope, num_splits, workspace, out, lse, dev_status, stream=None):
     """lvq_decode_attention for groups of requests whose first coded tokens are the same: group i holds
     the requests group_begin[i] .. group_begin[i + 1] - 1 and shares group_tokens[i] coded tokens, which
-    are restored once for all of them.  group_begin: int32 [n_groups + 1], group_tokens: int32 [n_groups],
+    are restored once for every 16 (request, query head) rows of a KV head.  group_begin: int32 [n_groups + 1], group_tokens: int32 [n_groups],
     both on the device.  num_splits = 0: the library's choice."""
     d, hq, dev = cfg.head_dim, cfg.n_q_heads, torch.cuda.current_device()
     n_groups = 0 if group_tokens is None else group_tokens.numel()
