@@ -51,7 +51,9 @@ Geo make_geo(const lvq_config* c) {
   const int max_coded = c->max_ctx > c->n_sink ? c->max_ctx - c->n_sink : 0;
   g.P = max_coded > 0 ? (max_coded + kPage - 1) / kPage : 1;
   g.B = c->max_batch; g.max_ctx = c->max_ctx; g.max_splits = c->max_splits;
-  g.RC = max((c->max_ctx + kPage - 1) / kPage, 64) + 16;   // rows cover offsets up to 512 positions
+  // every position, and offsets up to a decode chunk's 480 positions (factors of positions past max_ctx are not in
+  // the table: decode_first_position)
+  g.RC = max((c->max_ctx + kPage - 1) / kPage, 64) + 16;
   g.page_bytes = g.ng * kPage;
   g.wait_iters = debug_wait_iters;
   g.fault = debug_fault;

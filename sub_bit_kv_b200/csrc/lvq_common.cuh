@@ -80,6 +80,16 @@ __host__ __device__ inline size_t ws_partial_floats(const Geo& g) {
   return (size_t)g.B * g.Hq * g.max_splits * 2 * (g.d + 2);
 }
 
+// Decode attention: a chunk is kDecodePagesPerWarp pages of each of its kDecodeWarps compute warps.
+constexpr int kDecodeWarps = 15, kDecodePagesPerWarp = 4;
+// Position whose RoPE factors a compute lane of `warp`, token phase `phase`, starts from, in a split that begins at
+// coded token n0.  Past the split's end (its tokens are masked) it may lie past max_ctx by most of a chunk, more than
+// the table has rows for: any position inside does.
+__host__ __device__ inline int decode_first_position(const Geo& g, int n0, int warp, int phase) {
+  const int p = g.S + n0 + kPage * kDecodePagesPerWarp * warp + phase;
+  return p < g.max_ctx ? p : g.max_ctx - 1;
+}
+
 // Records the first device-side error: later errors do not overwrite it.
 __device__ inline void set_status(int32_t* st, int code) {
   if (st) atomicCAS(st, 0, code);

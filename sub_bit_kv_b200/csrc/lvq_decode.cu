@@ -54,10 +54,10 @@
 
 namespace lvq {
 
-constexpr int kCW = 15;                      // compute warps (+1 producer: 512 threads, 128 registers)
+constexpr int kCW = kDecodeWarps;            // 15 compute warps (+1 producer: 512 threads, 128 registers)
 constexpr int kCT = 32 * kCW;                // compute threads
 constexpr int kThr = kCT + 32;
-constexpr int kPPW = 4;                      // pages per warp per chunk
+constexpr int kPPW = kDecodePagesPerWarp;    // 4 pages per warp per chunk
 constexpr int kChunk = kPage * kCW * kPPW;   // 480 coded tokens per chunk
 constexpr int kStages = 3;
 constexpr int kSmemMax = 227 * 1024;
@@ -989,7 +989,7 @@ __global__ void __launch_bounds__(kThr, 1) decode_kernel(
   // overlaps the prologue
   float2 rf[X::CL];
   if (!producer && do_coded) {
-    const int p_first = g.S + n0 + kPage * kPPW * warp + lane / X::NPV;
+    const int p_first = decode_first_position(g, n0, warp, lane / X::NPV);
     const int f0 = lane_f0<D, C>(lane);
 #pragma unroll
     for (int e = 0; e < X::CL; ++e) rf[e] = rope_at(rope, g.RC, F, p_first, f0 + e);
@@ -1575,7 +1575,7 @@ __global__ void __launch_bounds__(kThr, 1) decode_runs_kernel(
       // a compute lane's RoPE factors at its first coded token
       float2 rf[X::CL];
       if (e.do_coded) {
-        const int p_first = g.S + n0 + kPage * kPPW * warp + lane / X::NPV;
+        const int p_first = decode_first_position(g, n0, warp, lane / X::NPV);
 #pragma unroll
         for (int c2 = 0; c2 < X::CL; ++c2) rf[c2] = rope_at(rope, g.RC, F, p_first, L.f0 + c2);
       }
